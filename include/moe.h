@@ -473,6 +473,56 @@ moe_status_t moe_permute_quantize_fp8(const void* x, int64_t T, int64_t H, int b
                                       int64_t n_rows, const int32_t* slot_pos, void* out_q,
                                       float* out_scales, void* stream);
 
+/* ------------------------------------------------------------ RMS norm
+ * The root-mean-square norm that stands in front of an MoE layer, with the
+ * addition of the residual stream in front of it.  (The pages begin at the
+ * router; this is the pre-norm of the block that the layer sits in.)
+ *   h = round(x + residual)             stored in residual_out; h = x if
+ *                                       residual is NULL (residual_out unused)
+ *   out = h * r * weight,  r = 1 / sqrt(mean over the row of h^2 + eps)
+ * in float32, each output rounded once; the norm is that of h as stored.
+ *   x, residual, residual_out, out [T,H] (dtype: MOE_F32 or MOE_BF16);
+ *   weight [H] (weight_dtype: MOE_F32 or MOE_BF16); eps >= 0.
+ * residual_out and out may each be x or residual itself (the stream updated in
+ * place), but not one another; no other overlap.  Any H and alignment; H a
+ * multiple of 8 with 16-byte aligned pointers takes the vectorised path.
+ *
+ * moe_rmsnorm_quantize_fp8: the same norm with the output quantized as
+ * moe_quantize_fp8 does, from the float32 values (not from bf16 ones): per
+ * block of `block` (32, 64, 128 or 256) elements scale = amax / 448 (1 for an
+ * all-zero block) and x_q = e4m3(y / scale).  x_q [T,H] e4m3 bytes, scales
+ * [T, H/block] float.  H a multiple of block (else MOE_ERR_INVALID_ARG) and at
+ * most 32768 (else MOE_ERR_UNSUPPORTED); x, residual, weight and residual_out
+ * 16-byte, x_q 8-byte, scales 4-byte aligned (else MOE_ERR_INVALID_ARG).
+ * residual_out may be x or residual itself. */
+moe_status_t moe_rmsnorm(const void* x, const void* residual, moe_dtype_t dtype,
+                         const void* weight, moe_dtype_t weight_dtype, int64_t T, int64_t H,
+                         float eps, void* residual_out, void* out, void* stream);
+
+moe_status_t moe_rmsnorm_quantize_fp8(const void* x, const void* residual, moe_dtype_t dtype,
+                                      const void* weight, moe_dtype_t weight_dtype, int64_t T,
+                                      int64_t H, float eps, int block, void* residual_out,
+                                      void* x_q, float* scales, void* stream);
+
+/* moe_rmsnorm_backward: with grad_y the gradient of out, and grad_h (NULL:
+ * none) the gradient that reaches h past the norm, on the residual stream:
+ *   grad_x = r (grad_y w) - h r^3 mean(grad_y w h) + grad_h   (rounded once)
+ *   grad_weight = sum over the rows of grad_y h r             (float32)
+ * grad_x is the gradient of x and of residual alike.  h is what moe_rmsnorm
+ * stored (residual_out, or x without a residual).
+ *   grad_y, grad_h, h, grad_x [T,H] (dtype); grad_weight [H] float, written
+ *   completely (zeros for T = 0), in an order that only T, H and the
+ *   alignment decide.
+ * grad_x may be grad_y, grad_h or h itself; no other overlap.  Workspace:
+ * moe_rmsnorm_backward_workspace_size(T, H) bytes, which may hold anything. */
+moe_status_t moe_rmsnorm_backward_workspace_size(int64_t T, int64_t H, size_t* bytes);
+
+moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const void* h,
+                                  moe_dtype_t dtype, const void* weight,
+                                  moe_dtype_t weight_dtype, int64_t T, int64_t H, float eps,
+                                  void* grad_x, float* grad_weight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------- workspace status word
  * Waits for `stream`, then reads the status a previous call left in
  * `workspace`: MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_TIMEOUT.  Each call

@@ -31,7 +31,8 @@ __all__ = [
     "moe_fill_pad_rows", "moe_quantize_fp8", "moe_dequantize_fp8", "moe_permute_fp8",
     "moe_route_backward", "moe_grouped_swiglu_save", "moe_grouped_swiglu_dgrad",
     "moe_grouped_swiglu_wgrad", "MOE_STATUS_WORKSPACE_BYTES", "moe_selftest_timeout",
-    "moe_permute_quantize_fp8",
+    "moe_permute_quantize_fp8", "moe_rmsnorm", "moe_rmsnorm_quantize_fp8",
+    "moe_rmsnorm_backward_workspace_size", "moe_rmsnorm_backward",
 ]
 
 # Bytes of the status-only workspace of the grouped SwiGLU training calls.
@@ -108,6 +109,12 @@ def load_library():
             "moe_grouped_swiglu_save": ([P, P, P, P, I64, I, I64, I64, P, P, P, P, SZ, P], I),
             "moe_grouped_swiglu_dgrad": ([P, P, P, P, P, I64, I, I64, I64, P, P, P, SZ, P], I),
             "moe_grouped_swiglu_wgrad": ([P, P, P, P, P, I64, I, I64, I64, P, P, P, SZ, P], I),
+            "moe_rmsnorm": ([P, P, I, P, I, I64, I64, ctypes.c_float, P, P, P], I),
+            "moe_rmsnorm_quantize_fp8": ([P, P, I, P, I, I64, I64, ctypes.c_float, I, P, P, P, P],
+                                         I),
+            "moe_rmsnorm_backward_workspace_size": ([I64, I64, PSZ], I),
+            "moe_rmsnorm_backward": ([P, P, P, I, P, I, I64, I64, ctypes.c_float, P, P, P, SZ, P],
+                                     I),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(lib, name)
@@ -178,6 +185,48 @@ def _workspace(nbytes, like, given):
             raise ValueError(f"workspace needs {nbytes} bytes, got {given.numel()}")
         return given
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=like.device)
+
+
+class _Target:
+    """Where a call runs: checks that every tensor lies on the current device,
+    and allocates outputs and workspaces for the stream that the kernels run
+    on (a tensor of another stream's pool could still be in use there)."""
+
+    def __init__(self, stream, like):
+        self.device = like.device
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {self.device}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        self.stream = stream
+        self.handle = _stream(stream)
+
+    def check(self, **tensors):
+        for name, t in tensors.items():
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, nbytes, given):
+        if given is None:
+            return self.empty((nbytes,), torch.uint8)
+        _cuda(given, "workspace", torch.uint8)
+        self.check(workspace=given)
+        if given.numel() < nbytes:
+            raise ValueError(f"workspace needs {nbytes} bytes, got {given.numel()}")
+        return given
+
+
+def _given(t, name, shape, dtype):
+    """A caller's output buffer, checked."""
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
 
 
 # -------------------------------------------------------------------- route
@@ -790,6 +839,108 @@ def moe_grouped_swiglu_wgrad(x: torch.Tensor, hidden: torch.Tensor, dy: torch.Te
         if t is not None:
             t._moe_workspace = ws
     return dw_up, dw_down
+
+
+# ------------------------------------------------------------------ RMS norm
+
+def _norm_args(x, weight, residual, residual_out, stream):
+    dt = _act(x, "x")
+    _cuda(weight, "weight", ndim=1)
+    if weight.dtype not in _DT:
+        raise ValueError(f"weight must be float32 or bfloat16, got {weight.dtype}")
+    if weight.shape[0] != x.shape[1]:
+        raise ValueError("weight must have H elements")
+    t = _Target(stream, x)
+    t.check(weight=weight)
+    if residual is not None:
+        _given(residual, "residual", x.shape, x.dtype)
+        t.check(residual=residual)
+        if residual_out is None:
+            residual_out = t.empty(x.shape, x.dtype)
+        else:
+            _given(residual_out, "residual_out", x.shape, x.dtype)
+            t.check(residual_out=residual_out)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    return t, dt, _DT[weight.dtype], residual_out
+
+
+def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                residual_out: Optional[torch.Tensor] = None, stream=None):
+    """(y, h): h = x + residual as stored (x itself without a residual) and
+    y = h / sqrt(mean(h^2) + eps) * weight.  out and residual_out may each be
+    x or residual (the stream updated in place), but not the same tensor."""
+    t, dt, wdt, residual_out = _norm_args(x, weight, residual, residual_out, stream)
+    T, H = x.shape
+    if out is None:
+        out = t.empty((T, H), x.dtype)
+    else:
+        _given(out, "out", (T, H), x.dtype)
+        t.check(out=out)
+    _ok("moe_rmsnorm", load_library().moe_rmsnorm(
+        _p(x), _p(residual), dt, _p(weight), wdt, T, H, eps, _p(residual_out), _p(out), t.handle))
+    return out, x if residual is None else residual_out
+
+
+def moe_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor,
+                             residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                             block: int = 128, out=None,
+                             residual_out: Optional[torch.Tensor] = None, stream=None):
+    """(x_q float8_e4m3fn [T,H], scales float32 [T,H/block], h): moe_rmsnorm
+    with y quantized from float32 as moe_quantize_fp8 does; out: an optional
+    (x_q, scales) pair to write into."""
+    t, dt, wdt, residual_out = _norm_args(x, weight, residual, residual_out, stream)
+    T, H = x.shape
+    if block <= 0 or H % block != 0:
+        raise ValueError("H must be a multiple of block")
+    if out is None:
+        q, sc = t.empty((T, H), torch.float8_e4m3fn), t.empty((T, H // block), torch.float32)
+    else:
+        q, sc = out
+        _given(q, "x_q", (T, H), torch.float8_e4m3fn)
+        _given(sc, "scales", (T, H // block), torch.float32)
+        t.check(x_q=q, scales=sc)
+    _ok("moe_rmsnorm_quantize_fp8", load_library().moe_rmsnorm_quantize_fp8(
+        _p(x), _p(residual), dt, _p(weight), wdt, T, H, eps, block, _p(residual_out), _p(q),
+        _p(sc), t.handle))
+    return q, sc, x if residual is None else residual_out
+
+
+def moe_rmsnorm_backward_workspace_size(T: int, H: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok("moe_rmsnorm_backward_workspace_size",
+        load_library().moe_rmsnorm_backward_workspace_size(T, H, ctypes.byref(n)))
+    return n.value
+
+
+def moe_rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                         grad_h: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                         grad_x: Optional[torch.Tensor] = None,
+                         grad_weight: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """(grad_x, grad_weight float32 [H]) of moe_rmsnorm from the h it returned;
+    grad_h is the gradient of h from the residual stream.  grad_x, which is
+    the gradient of x and of residual, may be grad_y, grad_h or h."""
+    t, dt, wdt, _ = _norm_args(h, weight, None, None, stream)
+    T, H = h.shape
+    for g, name in ((grad_y, "grad_y"), (grad_h, "grad_h"), (grad_x, "grad_x")):
+        if g is not None:
+            _given(g, name, (T, H), h.dtype)
+    if grad_y is None:
+        raise ValueError("grad_y is needed")
+    t.check(grad_y=grad_y, grad_h=grad_h, grad_x=grad_x, grad_weight=grad_weight)
+    if grad_x is None:
+        grad_x = t.empty((T, H), h.dtype)
+    if grad_weight is None:
+        grad_weight = t.empty((H,), torch.float32)
+    else:
+        _given(grad_weight, "grad_weight", (H,), torch.float32)
+    ws = t.workspace(moe_rmsnorm_backward_workspace_size(T, H), workspace)
+    _ok("moe_rmsnorm_backward", load_library().moe_rmsnorm_backward(
+        _p(grad_y), _p(grad_h), _p(h), dt, _p(weight), wdt, T, H, eps, _p(grad_x),
+        _p(grad_weight), _p(ws), ws.numel(), t.handle))
+    return grad_x, grad_weight
 
 
 def moe_workspace_status(workspace: torch.Tensor, stream=None) -> int:
