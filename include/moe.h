@@ -523,6 +523,52 @@ moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const 
                                   void* grad_x, float* grad_weight, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------- whole layer for few tokens
+ * Route, expert FFN and combine of up to MOE_LAYER_DECODE_MAX_TOKENS tokens
+ * (a decode step) in two launches, from the same packed weights as
+ * moe_grouped_swiglu ([MOE-OPS] §3, §8, §16; [COMBINE] §1):
+ *   out[t] = sum_{j=0..k-1} topk_w[t,j] * y(t, topk_idx[t,j])
+ *   y(t,e) = (silu(x_t @ w_gate[e]) * (x_t @ w_up[e])) @ w_down[e]
+ * Products are summed in float32, the hidden activation keeps at least 16
+ * bits, slots are added in slot order and out [T,H] bf16 is rounded once.  The
+ * result does not depend on scheduling, nor on the other tokens of the batch
+ * beyond the order of float32 sums that the shapes fix.
+ *
+ * moe_layer_decode chooses as moe_route does (the k largest logits, ties to
+ * the lower id, softmax over those k) and writes topk_idx [T,k] int32 and
+ * topk_w [T,k] float.
+ * moe_layer_decode_indices takes the choices: topk_idx [T,k] (-1 = empty slot;
+ * a token without any gets a zero row) and topk_w [T,k].  An id outside
+ * [-1, E), or one that its token names a second time, counts as empty and
+ * leaves MOE_ERR_DEVICE_CHECK in the workspace status.
+ *
+ * x [T,H]: bf16 if x_scales is NULL; else e4m3 codes with x_scales
+ * [T, H/128] float (block = 128, as moe_rmsnorm_quantize_fp8 and
+ * moe_quantize_fp8 leave them), standing for code * scale.
+ * w_up_packed [E,2I,H], w_down_packed [E,H,I]: moe_grouped_swiglu_pack's.
+ * Shapes: T <= 64, H a multiple of 256, I of 128, 1 <= k <= min(E, 32),
+ * E <= 1024 (else MOE_ERR_UNSUPPORTED); x, weights and out 16-byte aligned
+ * (else MOE_ERR_INVALID_ARG).  out must not overlap x.  Workspace:
+ * moe_layer_decode_workspace_size bytes, which may hold anything; calls that
+ * share one must not overlap on the GPU. */
+#define MOE_LAYER_DECODE_MAX_TOKENS 64
+
+moe_status_t moe_layer_decode_workspace_size(int64_t T, int E, int k, int64_t H, int64_t I,
+                                             size_t* bytes);
+
+moe_status_t moe_layer_decode(const void* x, const float* x_scales, const float* logits,
+                              int64_t T, int E, int k, int64_t H, int64_t I,
+                              const void* w_up_packed, const void* w_down_packed,
+                              int32_t* topk_idx, float* topk_w, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+moe_status_t moe_layer_decode_indices(const void* x, const float* x_scales,
+                                      const int32_t* topk_idx, const float* topk_w, int64_t T,
+                                      int E, int k, int64_t H, int64_t I,
+                                      const void* w_up_packed, const void* w_down_packed,
+                                      void* out, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
 /* ------------------------------------------------- workspace status word
  * Waits for `stream`, then reads the status a previous call left in
  * `workspace`: MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_TIMEOUT.  Each call

@@ -33,7 +33,12 @@ __all__ = [
     "moe_grouped_swiglu_wgrad", "MOE_STATUS_WORKSPACE_BYTES", "moe_selftest_timeout",
     "moe_permute_quantize_fp8", "moe_rmsnorm", "moe_rmsnorm_quantize_fp8",
     "moe_rmsnorm_backward_workspace_size", "moe_rmsnorm_backward",
+    "MOE_LAYER_DECODE_MAX_TOKENS", "moe_layer_decode_workspace_size", "moe_layer_decode",
+    "moe_layer_decode_indices",
 ]
+
+# The most tokens of moe_layer_decode.
+MOE_LAYER_DECODE_MAX_TOKENS = 64
 
 # Bytes of the status-only workspace of the grouped SwiGLU training calls.
 MOE_STATUS_WORKSPACE_BYTES = 256
@@ -115,6 +120,9 @@ def load_library():
             "moe_rmsnorm_backward_workspace_size": ([I64, I64, PSZ], I),
             "moe_rmsnorm_backward": ([P, P, P, I, P, I, I64, I64, ctypes.c_float, P, P, P, SZ, P],
                                      I),
+            "moe_layer_decode_workspace_size": ([I64, I, I, I64, I64, PSZ], I),
+            "moe_layer_decode": ([P, P, P, I64, I, I, I64, I64, P, P, P, P, P, P, SZ, P], I),
+            "moe_layer_decode_indices": ([P, P, P, P, I64, I, I, I64, I64, P, P, P, P, SZ, P], I),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(lib, name)
@@ -941,6 +949,80 @@ def moe_rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Te
         _p(grad_y), _p(grad_h), _p(h), dt, _p(weight), wdt, T, H, eps, _p(grad_x),
         _p(grad_weight), _p(ws), ws.numel(), t.handle))
     return grad_x, grad_weight
+
+
+# ------------------------------------------------- whole layer, few tokens
+
+def moe_layer_decode_workspace_size(T: int, E: int, k: int, H: int, I: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok("moe_layer_decode_workspace_size",
+        load_library().moe_layer_decode_workspace_size(T, E, k, H, I, ctypes.byref(n)))
+    return n.value
+
+
+def _layer_args(x, x_scales, w_up_packed, w_down_packed, out, stream):
+    if x_scales is None:
+        _cuda(x, "x", torch.bfloat16, 2)
+    else:
+        _cuda(x, "x", torch.float8_e4m3fn, 2)
+    T, H = x.shape
+    _cuda(w_up_packed, "w_up_packed", torch.bfloat16, 3)
+    _cuda(w_down_packed, "w_down_packed", torch.bfloat16, 3)
+    E, I2, H2 = w_up_packed.shape
+    I = I2 // 2
+    if H2 != H or I2 != 2 * I or tuple(w_down_packed.shape) != (E, H, I):
+        raise ValueError("packed weights do not match x")
+    if x_scales is not None:
+        if H % 128:
+            raise ValueError("H must be a multiple of the block of 128")
+        _given(x_scales, "x_scales", (T, H // 128), torch.float32)
+    t = _Target(stream, x)
+    t.check(x_scales=x_scales, w_up_packed=w_up_packed, w_down_packed=w_down_packed, out=out)
+    if out is None:
+        out = t.empty((T, H), torch.bfloat16)
+    else:
+        _given(out, "out", (T, H), torch.bfloat16)
+    return t, T, H, E, I, out
+
+
+def moe_layer_decode(x: torch.Tensor, logits: torch.Tensor, k: int, w_up_packed: torch.Tensor,
+                     w_down_packed: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None):
+    """(out [T,H] bf16, topk_idx, topk_w): a whole MoE layer for up to 64
+    tokens, from the router's logits [T,E].  x is bf16, or e4m3 with x_scales
+    [T, H/128]; the weights are moe_grouped_swiglu_pack's."""
+    t, T, H, E, I, out = _layer_args(x, x_scales, w_up_packed, w_down_packed, out, stream)
+    _given(logits, "logits", (T, E), torch.float32)
+    t.check(logits=logits)
+    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace)
+    idx, w = t.empty((T, k), torch.int32), t.empty((T, k), torch.float32)
+    _ok("moe_layer_decode", load_library().moe_layer_decode(
+        _p(x), _p(x_scales), _p(logits), T, E, k, H, I, _p(w_up_packed), _p(w_down_packed),
+        _p(idx), _p(w), _p(out), _p(ws), ws.numel(), t.handle))
+    out._moe_workspace = ws
+    return out, idx, w
+
+
+def moe_layer_decode_indices(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                             w_up_packed: torch.Tensor, w_down_packed: torch.Tensor,
+                             x_scales: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [T,H] bf16 of moe_layer_decode for given choices (-1 = empty slot)."""
+    t, T, H, E, I, out = _layer_args(x, x_scales, w_up_packed, w_down_packed, out, stream)
+    _cuda(topk_idx, "topk_idx", torch.int32, 2)
+    if topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must have one row per token")
+    k = topk_idx.shape[1]
+    _given(topk_w, "topk_w", (T, k), torch.float32)
+    t.check(topk_idx=topk_idx, topk_w=topk_w)
+    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace)
+    _ok("moe_layer_decode_indices", load_library().moe_layer_decode_indices(
+        _p(x), _p(x_scales), _p(topk_idx), _p(topk_w), T, E, k, H, I, _p(w_up_packed),
+        _p(w_down_packed), _p(out), _p(ws), ws.numel(), t.handle))
+    out._moe_workspace = ws
+    return out
 
 
 def moe_workspace_status(workspace: torch.Tensor, stream=None) -> int:
