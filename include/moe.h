@@ -531,8 +531,7 @@ moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const 
  *   y(t,e) = (silu(x_t @ w_gate[e]) * (x_t @ w_up[e])) @ w_down[e]
  * Products are summed in float32, the hidden activation keeps at least 16
  * bits, slots are added in slot order and out [T,H] bf16 is rounded once.  The
- * result does not depend on scheduling, nor on the other tokens of the batch
- * beyond the order of float32 sums that the shapes fix.
+ * same inputs give the same bits on every call.
  *
  * moe_layer_decode chooses as moe_route does (the k largest logits, ties to
  * the lower id, softmax over those k) and writes topk_idx [T,k] int32 and
