@@ -525,7 +525,7 @@ moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const 
 
 /* ---------------------------------------------- whole layer for few tokens
  * Route, expert FFN and combine of up to MOE_LAYER_DECODE_MAX_TOKENS tokens
- * (a decode step) in two launches, from the same packed weights as
+ * (a decode step) from the same packed weights as
  * moe_grouped_swiglu ([MOE-OPS] §3, §8, §16; [COMBINE] §1):
  *   out[t] = sum_{j=0..k-1} topk_w[t,j] * y(t, topk_idx[t,j])
  *   y(t,e) = (silu(x_t @ w_gate[e]) * (x_t @ w_up[e])) @ w_down[e]

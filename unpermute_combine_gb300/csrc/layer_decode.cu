@@ -6,11 +6,11 @@
 // With up to 64 tokens a layer is bound by reading the weights of the experts
 // that some token chose, once: 6 H I bytes each.  Two kernels stream them, the
 // up projections and then the down projections, through the tensor cores with
-// the operands swapped: 128 weight rows are the A tile (M = 128) and the few
-// tokens of an expert the B tile (N = 16, 32, 48 or 64), so no part of the tile
-// is padding that has to be read, and the weights go from TMA to shared memory
-// to tcgen05.mma without passing a register.
-//   warp 0       TMA producer: stages of 128 weight rows x 64 (16 KB) in a ring
+// the operands swapped: up to 128 weight rows are the A tile (M = 128) and a
+// group of up to 64 tokens of one expert the B tile (N), so nothing that is read
+// is padding, and the weights go from TMA to shared memory to tcgen05.mma
+// without passing a register.  A third, small kernel adds a token's slots up.
+//   warp 0       TMA producer: stages of weight rows x 64 or 128 of K, in a ring
 //                that fills half of the SM's shared memory, so that two blocks
 //                of either kernel fit an SM
 //   warp 1       one thread issues the MMAs
@@ -20,14 +20,13 @@
 //   warps 6..9   epilogue: silu(gate) * up, or the down products
 // Precision: the MMA's operands are bf16, but a hidden value, and an e4m3 code
 // times its scale, are not bf16 values.  Both are split into a bf16 value and
-// the bf16 value of the rest (16 bits together) and take two MMAs into the same
-// accumulator; the tensor cores idle here, so the second one costs nothing.
+// the bf16 value of the rest (16 bits together), which stand side by side as
+// columns of one B tile; the epilogue adds the two columns.  An MMA this narrow
+// takes as long as its A tile, so the second part costs next to nothing.
 // The second kernel is launched to overlap the first (programmatic dependent
 // launch): its blocks take the place of blocks that finish, and stream the down
 // projections, which do not depend on the first kernel, until their rings are
 // full; only then do they wait for it.
-// The last block to finish a strip of 128 output columns adds a token's slots
-// up, in slot order, so the result does not depend on which block that is.
 // Every block works the routing out for itself (top-k, softmax, each expert's
 // tokens) in shared memory: 64 tokens are too few for a launch of their own.
 // Every wait on an mbarrier is bounded; one that gives up records
@@ -38,18 +37,16 @@ namespace moe {
 namespace {
 
 constexpr int kMaxTokens = 64;
-constexpr int kM = 128;                   // weight rows of one tile
-constexpr int kK = 64;                    // K of a stage: one 128-byte swizzle row
-constexpr int kBox = 64;                  // weight rows of one TMA box
-constexpr int kTileBytes = kM * kK * 2;
-constexpr int kUpCols = 64;               // hidden columns of an up tile: 64 gate + 64 up rows
-constexpr int kMaxStages = 8;
+constexpr int kM = 128;                   // rows of an MMA, weight rows of a down tile
+constexpr int kBigBox = 64, kSmallBox = 16;    // weight rows of a TMA box
+constexpr int kMaxStages = 16;
 constexpr int kLoaders = 4;               // warps that fill B tiles
 constexpr int kThreads = 320;
-constexpr int kExchBytes = 16 * kUpCols * 4;   // up values on their way to the gate's threads
+constexpr int kExchBytes = 8 * 64 * 4;    // up values on their way to the gate's threads
 constexpr int kBlocksPerSm = 2;
-constexpr int kSmemBudget = 111 * 1024;   // dynamic shared memory of a block, two on an SM
+constexpr int kSmemBytes = 111 * 1024;    // dynamic shared memory of a block, two on an SM
 constexpr int kMaxParts = 8;              // splits of the down projections' K
+constexpr int kSumThreads = 128;
 
 struct LayerArgs {
     const void* x;              // bf16 [T,H], or e4m3 codes
@@ -61,33 +58,35 @@ struct LayerArgs {
     float* topk_w;
     uint16_t* out;              // [T,H] bf16
     WsHeader* header;
-    uint32_t* arrivals;         // [H / kM] products of a strip that are done
+    int* slots;                 // [2 + T*k]: units, slots in use, slot of each choice
+    float* weights;             // [T*k]
     uint16_t* hidden;           // [2][T*k, I] bf16: the values, and what they leave
     float* y;                   // [parts][slots, H]
     int T, E, k;
     int64_t H, I;
-    int nmax;                   // rows of a B tile: T rounded up to 16
-    int stages;
     int spread;                 // blocks that fit the GPU at once
+    uint32_t tmem_cols;
 };
 
 // ----------------------------------------------------------------- routing
 
 // What every block knows of the routing, in shared memory.  A slot is a row of
-// the workspace: experts in order, an expert's tokens in order.
+// the workspace: experts in order, an expert's tokens in order.  A unit is a
+// group of an expert's tokens that share a B tile.
 struct Routing {
     float* w;                   // [T*k]
     unsigned long long* mask;   // [E] tokens of each expert
     int16_t* slot;              // [T*k] slot of a choice, -1 = empty
     uint16_t* first;            // [E] first slot of each expert
-    uint16_t* active;           // [min(E, T*k)] experts with tokens
+    uint16_t* unit;             // [T*k] expert of each unit
+    uint8_t* group;             // [T*k] which group of the expert's tokens it is
     uint8_t* token;             // [T*k] token of each slot
-    int* count;                 // [3]: active experts, bad choices, slots
+    int* count;                 // [4]: units, bad choices, slots, tokens of a group
 };
 
 __host__ __device__ inline size_t routing_bytes(int T, int E, int k) {
     const size_t n = size_t(T) * k;
-    const size_t b = 16 + n * 4 + size_t(E) * 8 + n * 2 + size_t(E) * 2 + (size_t(E) + 1) * 2 + n;
+    const size_t b = 16 + size_t(E) * 8 + n * 4 + n * 2 + size_t(E) * 2 + n * 2 + n + n;
     return (b + 127) / 128 * 128;
 }
 
@@ -99,8 +98,9 @@ __device__ __forceinline__ Routing carve_routing(uint8_t* p, int T, int E, int k
     r.w = reinterpret_cast<float*>(r.mask + E);
     r.slot = reinterpret_cast<int16_t*>(r.w + n);
     r.first = reinterpret_cast<uint16_t*>(r.slot + n);
-    r.active = r.first + E;
-    r.token = reinterpret_cast<uint8_t*>(r.active + E + 1);
+    r.unit = r.first + E;
+    r.group = reinterpret_cast<uint8_t*>(r.unit + n);
+    r.token = r.group + n;
     return r;
 }
 
@@ -192,23 +192,41 @@ __device__ void route(const LayerArgs& a, const Routing& r, bool publish) {
     }
     __syncthreads();
     if (warp == 0) {
-        int slots = 0, act = 0;
+        // Tokens of a group: a large group keeps its rows' place in every stage
+        // and leaves less of the ring to weights, a small one reads the weights
+        // of an expert with more tokens again, from L2.  16, unless that is a
+        // tenth more reads; then 32, by the same rule; then 64.
+        int act = 0, by16 = 0, by32 = 0;
+        for (int e = lane; e < E; e += 32) {
+            const int c = __popcll(r.mask[e]);
+            act += c > 0;
+            by16 += (c + 15) / 16;
+            by32 += (c + 31) / 32;
+        }
+        act = __reduce_add_sync(0xFFFFFFFFu, act);
+        by16 = __reduce_add_sync(0xFFFFFFFFu, by16);
+        by32 = __reduce_add_sync(0xFFFFFFFFu, by32);
+        const int g = by16 * 10 <= act * 11 ? 16 : by32 * 10 <= act * 11 ? 32 : 64;
+        int slots = 0, units = 0;
         for (int base = 0; base < E; base += 32) {
             const int e = base + lane;
-            const int c = e < E ? __popcll(r.mask[e]) : 0;
-            int incl = c;
+            const int c = e < E ? __popcll(r.mask[e]) : 0, u = (c + g - 1) / g;
+            int both = c << 16 | u, incl = both;           // at most 2048 of each
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
                 if (lane >= o) incl += v;
             }
-            const unsigned some = __ballot_sync(0xFFFFFFFFu, c > 0);
-            if (e < E) r.first[e] = uint16_t(slots + incl - c);
-            if (c > 0) r.active[act + __popc(some & ((1u << lane) - 1u))] = uint16_t(e);
-            slots += __shfl_sync(0xFFFFFFFFu, incl, 31);
-            act += __popc(some);
+            if (e < E) r.first[e] = uint16_t(slots + (incl >> 16) - c);
+            for (int i = 0; i < u; ++i) {
+                r.unit[units + (incl & 0xFFFF) - u + i] = uint16_t(e);
+                r.group[units + (incl & 0xFFFF) - u + i] = uint8_t(i);
+            }
+            const int all = __shfl_sync(0xFFFFFFFFu, incl, 31);
+            slots += all >> 16;
+            units += all & 0xFFFF;
         }
-        if (lane == 0) { r.count[0] = act; r.count[2] = slots; }
+        if (lane == 0) { r.count[0] = units; r.count[2] = slots; r.count[3] = g; }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -224,50 +242,73 @@ __device__ void route(const LayerArgs& a, const Routing& r, bool publish) {
 
 // ------------------------------------------------------------------- tiles
 
-// One work item: the tile of 128 weight rows at `strip` of an expert, over the
-// stages [k0, k1) of its K.
-struct Item {
-    int e, first, n;            // expert, its first slot, its tokens
-    int strip, part, k0, k1;
+// How the routing is cut into work items, the same in every block.
+struct Work {
+    int units, strips, parts, items;
+    int cols;                   // up: hidden columns of a tile (as many gate and up rows)
+    int rows;                   // weight rows of a tile
+    int group, subs, steps;     // tokens of a B tile; sub-tiles of a stage; stages of K
+    int stage_bytes, stages;
 };
 
-struct Work { int act, strips, parts, steps, items; };
+// parts of the down projections' K, so that there is work for every block
+__device__ __forceinline__ int down_parts(const LayerArgs& a, int units) {
+    const int strips = int(a.H / kM), most = int(min64(kMaxParts, a.I / 128));
+    return units > 0 ? max(1, min(most, a.spread / (units * strips))) : 1;
+}
 
-template <bool kUp>
-__device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r) {
+template <bool kUp, bool kB2>
+__device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r, int ring_bytes) {
     Work w;
-    w.act = r.count[0];
-    w.strips = int(kUp ? a.I / kUpCols : a.H / kM);
-    w.steps = int((kUp ? a.H : a.I) / kK);
-    w.parts = 1;
-    // the down products are sums over K, which may be cut to give more blocks work
-    if (!kUp && w.act > 0)
-        w.parts = max(1, min(min(kMaxParts, w.steps / 2), a.spread / (w.act * w.strips)));
-    w.items = w.act * w.strips * w.parts;
+    w.units = r.count[0];
+    w.group = r.count[3];
+    w.parts = kUp ? 1 : down_parts(a, w.units);
+    // narrower up tiles where there are not enough wide ones for every block
+    w.cols = 64;
+    if (kUp)
+        while (w.cols > 16 && w.units * int(a.I / w.cols) * 4 < a.spread * 3) w.cols /= 2;
+    w.rows = kUp ? 2 * w.cols : kM;
+    w.strips = int(kUp ? a.I / w.cols : a.H / kM);
+    w.items = w.units * w.strips * w.parts;
+    // two sub-tiles a stage (256 bytes of a row) where three such stages fit
+    const int sub = (w.rows + w.group * (kB2 ? 2 : 1)) * 128;
+    const int left = ring_bytes - (kM - w.rows) * 128;     // an MMA reads kM rows all the same
+    w.subs = 6 * sub <= left ? 2 : 1;
+    w.stage_bytes = w.subs * sub;
+    w.stages = min(kMaxStages, left / w.stage_bytes);
+    w.steps = int((kUp ? a.H : a.I) / (64 * w.subs));
     return w;
 }
 
-// Up: an expert's strips one after the other.  Down: a strip's experts and
-// parts one after the other, so that strips finish, and are added up, early.
+// One work item: a tile of weight rows over the stages [k0, k1) of its K.
+struct Item {
+    int e, first, n;            // expert, the unit's first slot, its tokens
+    int strip, part, k0, k1;
+};
+
+// Up: a unit's strips one after the other.  Down: a strip's units and parts.
 template <bool kUp>
 __device__ __forceinline__ Item item_of(const Work& w, const Routing& r, int i) {
     Item it;
     const int q = kUp ? i : i / w.parts;
     it.part = kUp ? 0 : i % w.parts;
-    const int act = kUp ? q / w.strips : q % w.act;
-    it.strip = kUp ? q % w.strips : q / w.act;
-    it.e = r.active[act];
-    it.first = r.first[it.e];
-    it.n = __popcll(r.mask[it.e]);
+    const int unit = kUp ? q / w.strips : q % w.units;
+    it.strip = kUp ? q % w.strips : q / w.units;
+    it.e = r.unit[unit];
+    const int at = r.group[unit] * w.group;
+    it.first = r.first[it.e] + at;
+    it.n = min(w.group, __popcll(r.mask[it.e]) - at);
     it.k0 = it.part * w.steps / w.parts;
     it.k1 = (it.part + 1) * w.steps / w.parts;
     return it;
 }
 
-__device__ __forceinline__ int columns(int n) { return (n + 15) & ~15; }
+// B rows of n tokens: each part of two takes a multiple of 8, one alone of 16,
+// so that N is a multiple of 16.
+template <bool kB2>
+__device__ __forceinline__ int b_rows(int n) { return kB2 ? (n + 7) & ~7 : (n + 15) & ~15; }
 
-// A float's bf16 value, and the bf16 value of what that leaves (0 for an
-// infinity, so that it stays one).
+// What a float's bf16 value leaves of it (0 for an infinity, so that it stays one).
 __device__ __forceinline__ float bf16_rest(float v, float hi) {
     return (__float_as_uint(hi) & 0x7F800000u) == 0x7F800000u ? 0.0f : v - hi;
 }
@@ -284,11 +325,7 @@ __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-__device__ __forceinline__ uint4 ld_cg_v4(const void* p) {
-    return __ldcg(static_cast<const uint4*>(p));
-}
-
-// Chunk c (8 values of K) of B row `row` in a tile with 128-byte swizzle.
+// Chunk c (8 values of K) of a B row in a sub-tile with 128-byte swizzle.
 __device__ __forceinline__ void put_chunk(uint8_t* tile, int row, int c, uint4 v) {
     *reinterpret_cast<uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4)) = v;
 }
@@ -305,57 +342,29 @@ __device__ __forceinline__ bool any_epilogue(bool v) {
     return r != 0;
 }
 
-// out[t, strip] = sum over the slots, in order, of the weighted down products.
-// 128 threads: lane = 4 columns, warp = every fourth token.
-__device__ void add_up(const LayerArgs& a, const Routing& r, const Work& w, int strip) {
-    const int lane = int(lane_id());
-    const int64_t h = int64_t(strip) * kM + lane * 4, part = int64_t(r.count[2]) * a.H;
-    for (int t = (threadIdx.x >> 5) & 3; t < a.T; t += 4) {
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {
-            const int slot = r.slot[t * a.k + j];
-            if (slot < 0) continue;
-            const float* p = a.y + int64_t(slot) * a.H + h;
-            float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-            for (int q = 1; q < w.parts; ++q) {
-                const float4 o = __ldcg(reinterpret_cast<const float4*>(p + q * part));
-                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-            }
-            const float pw = r.w[t * a.k + j];
-            s.x = fmaf(pw, v.x, s.x);
-            s.y = fmaf(pw, v.y, s.y);
-            s.z = fmaf(pw, v.z, s.z);
-            s.w = fmaf(pw, v.w, s.w);
-        }
-        *reinterpret_cast<uint2*>(a.out + t * a.H + h) =
-            make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
-    }
-}
-
 // kUp: hidden = silu(x Wg^T) * (x Wu^T) of every active expert's tokens;
-// otherwise y = hidden Wd^T, and out.  kB2: the B rows come in two bf16 parts
-// (e4m3 x, or hidden rows).
+// otherwise y = hidden Wd^T.  kB2: the B rows come in two bf16 parts (e4m3 x,
+// or hidden rows).
 template <bool kUp, bool kB2>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
+layer_kernel(const __grid_constant__ CUtensorMap map_big,
+             const __grid_constant__ CUtensorMap map_small, const LayerArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_failed;
-    __shared__ int s_last;
 
     const int warp = threadIdx.x >> 5, lane = int(lane_id());
-    const int b_bytes = a.nmax * 128 * (kB2 ? 2 : 1), stage_bytes = kTileBytes + b_bytes;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    float* exch = reinterpret_cast<float*>(ring + a.stages * stage_bytes);     // [16][kUpCols]
-    const Routing r = carve_routing(ring + a.stages * stage_bytes + kExchBytes, a.T, a.E, a.k);
+    const int ring_bytes = kSmemBytes - 1024 - kExchBytes - int(routing_bytes(a.T, a.E, a.k));
+    float* exch = reinterpret_cast<float*>(ring + ring_bytes);                 // [8][cols]
+    const Routing r = carve_routing(ring + ring_bytes + kExchBytes, a.T, a.E, a.k);
 
     if (threadIdx.x == 0) {
         s_failed = 0;
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_addr(&full_a[s]), 1);
             mbar_init(smem_addr(&full_b[s]), 1);
             mbar_init(smem_addr(&empty[s]), 1);
@@ -366,32 +375,30 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
         }
         mbar_fence_init();
     }
-    // two accumulators of nmax fp32 columns, a power of two of at least 32
-    const uint32_t tmem_cols = a.nmax <= 16 ? 32u : a.nmax <= 32 ? 64u : 128u;
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     :: "r"(smem_addr(&s_tmem)), "r"(tmem_cols) : "memory");
+                     :: "r"(smem_addr(&s_tmem)), "r"(a.tmem_cols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     route(a, r, kUp && a.logits && blockIdx.x == 0);       // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const Work w = work_of<kUp>(a, r);
-    if (kUp) {
-        // every block of this kernel is resident and has its tensor memory
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (blockIdx.x == 0) {
-            if (threadIdx.x == 0) {
-                a.header->status = r.count[1] ? MOE_ERR_DEVICE_CHECK : MOE_OK;
-                a.header->detail = 0;
-            }
-            for (int64_t i = threadIdx.x; i < a.H / kM; i += blockDim.x) a.arrivals[i] = 0u;
+    const Work w = work_of<kUp, kB2>(a, r, ring_bytes);
+    const int b_sub = w.group * (kB2 ? 2 : 1) * 128, a_sub = w.rows * 128;
+    // every block of this kernel is resident and has its tensor memory
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (kUp && blockIdx.x == 0) {                          // for the sum over slots
+        if (threadIdx.x == 0) {
+            a.header->status = r.count[1] ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+            a.header->detail = 0;
+            a.slots[0] = w.units;
+            a.slots[1] = r.count[2];
         }
-    } else if (w.items == 0) {                             // every slot is empty
-        for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < a.T * a.H;
-             i += int64_t(gridDim.x) * kThreads)
-            a.out[i] = 0;
+        for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+            a.slots[2 + i] = r.slot[i];
+            a.weights[i] = r.w[i];
+        }
     }
 
     if (warp == 0) {
@@ -400,26 +407,37 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
             uint32_t it = 0;
             for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x) {
                 const Item m = item_of<kUp>(w, r, i);
-                // the two boxes: 64 gate rows and the matching up rows, or 128 rows of Wd
-                const int row = kUp ? int(m.e * 2 * a.I) + m.strip / 2 * 256 + m.strip % 2 * 64
+                // gate rows and the matching up rows (blocks of 128 each), or rows of Wd
+                const int col = m.strip * w.cols;
+                const int row = kUp ? int(m.e * 2 * a.I) + col / 128 * 256 + col % 128
                                     : int(m.e * a.H) + m.strip * kM;
-                const int row2 = row + (kUp ? 128 : kBox);
+                const int row2 = row + (kUp ? 128 : kM / 2), half = w.rows / 2;
                 for (int ks = m.k0; ks < m.k1; ++ks, ++it) {
-                    const int s = it % a.stages;
-                    const uint32_t turn = it / a.stages;
+                    const int s = it % w.stages;
+                    const uint32_t turn = it / w.stages;
                     if (!kUp && turn == 1 && s == 0) wait_for_predecessor();   // the ring is full
                     if (!mbar_wait(smem_addr(&empty[s]), (turn & 1u) ^ 1u)) { s_failed = 1; break; }
-                    const uint32_t dst = smem_addr(ring + s * stage_bytes);
                     const uint32_t bar = smem_addr(&full_a[s]);
-                    mbar_expect_tx(bar, kTileBytes);
-                    tma_load_2d(dst, &map_w, ks * kK, row, bar);
-                    tma_load_2d(dst + kTileBytes / 2, &map_w, ks * kK, row2, bar);
+                    mbar_expect_tx(bar, w.subs * a_sub);
+                    for (int u = 0; u < w.subs; ++u) {
+                        const uint32_t dst = smem_addr(ring + s * w.stage_bytes + u * a_sub);
+                        const int c = (ks * w.subs + u) * 64;
+                        if (half == kBigBox) {
+                            tma_load_2d(dst, &map_big, c, row, bar);
+                            tma_load_2d(dst + kBigBox * 128, &map_big, c, row2, bar);
+                        } else {
+                            for (int b = 0; b < half; b += kSmallBox) {
+                                tma_load_2d(dst + b * 128, &map_small, c, row + b, bar);
+                                tma_load_2d(dst + (half + b) * 128, &map_small, c, row2 + b, bar);
+                            }
+                        }
+                    }
                 }
             }
             // a block that gave up leaves no copy of its own in flight
             if (s_failed)
-                for (uint32_t b = it > uint32_t(a.stages) ? it - a.stages : 0; b < it; ++b)
-                    mbar_wait(smem_addr(&full_a[b % a.stages]), (b / a.stages) & 1u);
+                for (uint32_t b = it > uint32_t(w.stages) ? it - w.stages : 0; b < it; ++b)
+                    mbar_wait(smem_addr(&full_a[b % w.stages]), (b / w.stages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -428,23 +446,23 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
             uint32_t it = 0, tile = 0;
             for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x, ++tile) {
                 const Item m = item_of<kUp>(w, r, i);
-                const uint32_t idesc = idesc_bf16(kM, columns(m.n));
-                const uint32_t buf = tile & 1u, acc = tmem + buf * a.nmax;
+                const uint32_t idesc = idesc_bf16(kM, b_rows<kB2>(m.n) * (kB2 ? 2 : 1));
+                const uint32_t buf = tile & 1u, acc = tmem + buf * (a.tmem_cols / 2);
                 if (!mbar_wait(smem_addr(&acc_empty[buf]), ((tile >> 1) & 1u) ^ 1u)) { s_failed = 1; break; }
                 tc_fence_after();
                 for (int ks = m.k0; ks < m.k1; ++ks, ++it) {
-                    const int s = it % a.stages;
-                    const uint32_t ph = (it / a.stages) & 1u;
+                    const int s = it % w.stages;
+                    const uint32_t ph = (it / w.stages) & 1u;
                     if (!mbar_wait(smem_addr(&full_b[s]), ph) ||
                         !mbar_wait(smem_addr(&full_a[s]), ph)) { s_failed = 1; break; }
                     tc_fence_after();
-                    const uint32_t wa = smem_addr(ring + s * stage_bytes), xb = wa + kTileBytes;
+                    const uint32_t wa = smem_addr(ring + s * w.stage_bytes), xb = wa + w.subs * a_sub;
+                    for (int u = 0; u < w.subs; ++u) {
 #pragma unroll
-                    for (int kk = 0; kk < kK / 16; ++kk) {
-                        const uint64_t ad = smem_desc_k128(wa + kk * 32);
-                        mma_bf16(acc, ad, smem_desc_k128(xb + kk * 32), idesc, ks != m.k0 || kk);
-                        if (kB2)
-                            mma_bf16(acc, ad, smem_desc_k128(xb + a.nmax * 128 + kk * 32), idesc, 1);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16(acc, smem_desc_k128(wa + u * a_sub + kk * 32),
+                                     smem_desc_k128(xb + u * b_sub + kk * 32), idesc,
+                                     ks != m.k0 || u || kk);
                     }
                     mma_commit(smem_addr(&empty[s]));
                 }
@@ -458,16 +476,17 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
         // No more warps than stages: a warp that waits for a stage has seen the
         // use before its own last one end, so the stage's barrier can be at most
         // one phase behind and the parity is not mistaken for an older one.
-        const uint32_t loaders = min(kLoaders, a.stages), mine = warp - 2;
+        const uint32_t loaders = min(kLoaders, w.stages), mine = warp - 2;
+        const int row_chunks = 8 * w.subs, row_shift = w.subs == 2 ? 4 : 3;
         uint32_t it = 0;
         bool stop = false;                                 // the same in all lanes
         for (int i = blockIdx.x; i < w.items && !stop; i += gridDim.x) {
             const Item m = item_of<kUp>(w, r, i);
-            const int chunks = m.n * 8;
+            const int chunks = m.n * row_chunks, part2 = b_rows<kB2>(m.n) * 128;
             for (int ks = m.k0; ks < m.k1; ++ks, ++it) {
                 if (it % loaders != mine) continue;
-                const int s = it % a.stages;
-                uint8_t* tile = ring + s * stage_bytes + kTileBytes;
+                const int s = it % w.stages;
+                uint8_t* tile = ring + s * w.stage_bytes + w.subs * a_sub;
                 bool ready = false;
                 for (int c0 = 0; c0 < chunks; c0 += 128) {
                     // up to four chunks a lane in flight; the first ones before the wait
@@ -475,7 +494,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
                     float sc[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int c = c0 + q * 32 + lane, row = c >> 3, col = ks * kK + (c & 7) * 8;
+                        const int c = c0 + q * 32 + lane, row = c >> row_shift;
+                        const int col = (ks * row_chunks + (c & (row_chunks - 1))) * 8;
                         if (c >= chunks) continue;
                         if (kUp && !kB2) {
                             v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) +
@@ -489,17 +509,18 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
                             sc[q] = __ldg(a.x_scales + t * (a.H / 128) + col / 128);
                         } else {
                             const uint16_t* p = a.hidden + int64_t(m.first + row) * a.I + col;
-                            v[q] = ld_cg_v4(p);
-                            v2[q] = ld_cg_v4(p + int64_t(a.T) * a.k * a.I);
+                            v[q] = __ldcg(reinterpret_cast<const uint4*>(p));
+                            v2[q] = __ldcg(reinterpret_cast<const uint4*>(p + int64_t(a.T) * a.k * a.I));
                         }
                     }
                     if (!ready) {
-                        ready = mbar_wait(smem_addr(&empty[s]), ((it / a.stages) & 1u) ^ 1u);
+                        ready = mbar_wait(smem_addr(&empty[s]), ((it / w.stages) & 1u) ^ 1u);
                         if (!ready) { s_failed = 1; break; }
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int c = c0 + q * 32 + lane, row = c >> 3;
+                        const int c = c0 + q * 32 + lane, row = c >> row_shift;
+                        const int j = c & (row_chunks - 1);
                         if (c >= chunks) continue;
                         if (kUp && kB2) {
                             float f[8];
@@ -511,8 +532,9 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
                             for (int e = 0; e < 8; ++e) f[e] *= sc[q];
                             split8(f, v[q], v2[q]);
                         }
-                        put_chunk(tile, row, c & 7, v[q]);
-                        if (kB2) put_chunk(tile + a.nmax * 128, row, c & 7, v2[q]);
+                        uint8_t* sub = tile + (j >> 3) * b_sub;
+                        put_chunk(sub, row, j & 7, v[q]);
+                        if (kB2) put_chunk(sub + part2, row, j & 7, v2[q]);
                     }
                 }
                 // each thread orders its writes before the tensor core's reads
@@ -524,32 +546,39 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if (!kUp) wait_for_predecessor();                  // the arrival counts
-        const int q = warp & 3, row = q * 32 + lane;       // TMEM lane quadrant, weight row
+        if (!kUp) wait_for_predecessor();                  // y may still be read
+        const int q = warp & 3, row = q * 32 + lane;       // TMEM lane quadrant, tile row
         uint32_t tile = 0;
         for (int i = blockIdx.x; i < w.items; i += gridDim.x, ++tile) {
             const Item m = item_of<kUp>(w, r, i);
-            const uint32_t buf = tile & 1u, acc = tmem + buf * a.nmax + (uint32_t(q * 32) << 16);
+            const uint32_t buf = tile & 1u;
+            const uint32_t acc = tmem + buf * (a.tmem_cols / 2) + (uint32_t(q * 32) << 16);
             const bool ok = !s_failed && mbar_wait(smem_addr(&acc_full[buf]), (tile >> 1) & 1u);
             // all 128 threads go on, or none
             if (any_epilogue(!ok)) { s_failed = 1; break; }
             tc_fence_after();
-            for (int c0 = 0; c0 < m.n; c0 += 16) {
-                float v[16];
-                tmem_ld16(acc + c0, v);
-                if (kUp) {
-                    // rows 0-63 hold the gate, rows 64-127 the up values
-                    if (q >= 2) {
+            for (int c0 = 0; c0 < m.n; c0 += 8) {
+                float v[8];
+                tmem_ld8(acc + c0, v);
+                if (kB2) {
+                    float lo[8];
+                    tmem_ld8(acc + b_rows<kB2>(m.n) + c0, lo);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) exch[c * kUpCols + row - 64] = v[c];
+                    for (int c = 0; c < 8; ++c) v[c] += lo[c];
+                }
+                if (kUp) {
+                    // the tile's first rows hold the gate, the next ones the up values
+                    if (row >= w.cols && row < 2 * w.cols) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) exch[c * 64 + row - w.cols] = v[c];
                     }
                     bar_epilogue();
-                    if (q < 2) {
-                        uint16_t* hp = a.hidden + int64_t(m.first + c0) * a.I + m.strip * kUpCols + row;
+                    if (row < w.cols) {
+                        uint16_t* hp = a.hidden + int64_t(m.first + c0) * a.I + m.strip * w.cols + row;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
+                        for (int c = 0; c < 8; ++c) {
                             if (c0 + c >= m.n) break;
-                            const float h = v[c] / (1.0f + expf(-v[c])) * exch[c * kUpCols + row];
+                            const float h = v[c] / (1.0f + expf(-v[c])) * exch[c * 64 + row];
                             const uint16_t hi = f32_to_bf16_rn(h);
                             hp[c * a.I] = hi;
                             hp[(int64_t(a.T) * a.k + c) * a.I] =
@@ -561,22 +590,12 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
                     float* yp = a.y + (int64_t(m.part) * r.count[2] + m.first + c0) * a.H +
                                 m.strip * kM + row;
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < 8; ++c)
                         if (c0 + c < m.n) yp[c * a.H] = v[c];
                 }
             }
             tc_fence_before();
             mbar_arrive(smem_addr(&acc_empty[buf]));
-            if (!kUp) {
-                bar_epilogue();
-                if (row == 0) {
-                    __threadfence();
-                    s_last = atomicAdd(&a.arrivals[m.strip], 1u) == uint32_t(w.act * w.parts - 1);
-                    __threadfence();
-                }
-                bar_epilogue();
-                if (s_last) add_up(a, r, w, m.strip);
-            }
         }
     }
     tc_fence_before();
@@ -589,7 +608,44 @@ layer_kernel(const __grid_constant__ CUtensorMap map_w, const LayerArgs a) {
     __syncwarp();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
-                     :: "r"(tmem), "r"(tmem_cols) : "memory");
+                     :: "r"(tmem), "r"(a.tmem_cols) : "memory");
+}
+
+// out[t] = sum over the slots, in order, of the weighted down products.  A thread
+// has 4 columns of a token.
+__global__ void __launch_bounds__(kSumThreads) layer_sum_kernel(const LayerArgs a) {
+    __shared__ int s_slot[kMaxTopK];
+    __shared__ float s_w[kMaxTopK];
+    const int t = blockIdx.y;
+    const int64_t h = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 4;
+    wait_for_predecessor();
+    if (int(threadIdx.x) < a.k) {
+        s_slot[threadIdx.x] = __ldcg(a.slots + 2 + t * a.k + threadIdx.x);
+        s_w[threadIdx.x] = __ldcg(a.weights + t * a.k + threadIdx.x);
+    }
+    const int parts = down_parts(a, __ldcg(a.slots));
+    const int64_t part = int64_t(__ldcg(a.slots + 1)) * a.H;
+    __syncthreads();
+    if (h >= a.H) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int q = 0; q < parts; ++q) {
+#pragma unroll 8
+        for (int j = 0; j < a.k; ++j) {
+            const int slot = s_slot[j];
+            const float w = s_w[j];
+            // no branch around the load, so that eight of them are in flight
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.y + q * part +
+                                                                    int64_t(max(slot, 0)) * a.H + h));
+            if (slot >= 0) {
+                s.x = fmaf(w, v.x, s.x);
+                s.y = fmaf(w, v.y, s.y);
+                s.z = fmaf(w, v.z, s.z);
+                s.w = fmaf(w, v.w, s.w);
+            }
+        }
+    }
+    *reinterpret_cast<uint2*>(a.out + t * a.H + h) =
+        make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
 }
 
 // -------------------------------------------------------------------- host
@@ -605,43 +661,26 @@ moe_status_t check_layer(int64_t T, int E, int k, int64_t H, int64_t I) {
     return MOE_OK;
 }
 
-// Items that the down projections may be split into: a bound of the blocks that
-// any GPU of this kind holds at once.
+// Most blocks that the kernels are launched with, whatever the GPU: a bound of
+// the items that the down projections are split into.
 constexpr int64_t kSpread = 320;
 
-struct Layout { size_t arrivals, hidden, y, total; };
+struct Layout { size_t slots, weights, hidden, y, total; };
 
 Layout workspace_layout(int64_t T, int k, int64_t H, int64_t I) {
     const size_t n = size_t(T) * k;
     Layout l;
-    l.arrivals = kWsAlign;
-    l.hidden = l.arrivals + align_up(size_t(H / kM) * 4, kWsAlign);
+    l.slots = kWsAlign;
+    l.weights = l.slots + align_up((2 + n) * 4, kWsAlign);
+    l.hidden = l.weights + align_up(n * 4, kWsAlign);
     l.y = l.hidden + align_up(n * size_t(I) * 4, kWsAlign);
-    // unsplit: n rows of H; split: no more than kSpread strips of kM columns
-    // over at most T tokens of an expert (work_of)
+    // not split: n rows of H; split: kSpread items of at most T tokens and kM columns
     l.total = l.y + align_up(max64(int64_t(n) * H, T * kSpread * kM) * 4, kWsAlign);
     return l;
 }
 
-int stage_bytes(const LayerArgs& a, bool two_parts) {
-    return kTileBytes + a.nmax * 128 * (two_parts ? 2 : 1);
-}
-
-// As many stages as half of an SM's shared memory holds: 2 (64 tokens, 1024
-// experts, k = 32, two parts) to 8; 5 for up to 16 tokens.
-int ring_stages(const LayerArgs& a, bool two_parts) {
-    const int left = kSmemBudget - 1024 - kExchBytes - int(routing_bytes(a.T, a.E, a.k));
-    const int n = left / stage_bytes(a, two_parts);
-    return n < kMaxStages ? n : kMaxStages;
-}
-
-size_t smem_bytes(const LayerArgs& a, bool two_parts) {
-    return 1024 + size_t(a.stages) * stage_bytes(a, two_parts) + kExchBytes +
-           routing_bytes(a.T, a.E, a.k);
-}
-
-moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T, void* workspace, size_t workspace_bytes,
-                   cudaStream_t s) {
+moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T, void* workspace,
+                   size_t workspace_bytes, cudaStream_t s) {
     const moe_status_t st = check_layer(T, a.E, a.k, a.H, a.I);
     if (st != MOE_OK) return st;
     const Layout l = workspace_layout(T, a.k, a.H, a.I);
@@ -659,31 +698,41 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     if (T == 0)
         return cudaMemsetAsync(ws, 0, 8, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     a.T = int(T);
-    a.arrivals = reinterpret_cast<uint32_t*>(ws + l.arrivals);
+    a.slots = reinterpret_cast<int*>(ws + l.slots);
+    a.weights = reinterpret_cast<float*>(ws + l.weights);
     a.hidden = reinterpret_cast<uint16_t*>(ws + l.hidden);
     a.y = reinterpret_cast<float*>(ws + l.y);
-    a.nmax = (a.T + 15) / 16 * 16;
     a.spread = int(min64(int64_t(sm_count()) * kBlocksPerSm, kSpread));
 
-    CUtensorMap m_up, m_down;
-    if (!make_map(&m_up, w_up, int64_t(a.E) * 2 * a.I, a.H, kBox) ||
-        !make_map(&m_down, w_down, int64_t(a.E) * a.H, a.I, kBox))
+    CUtensorMap up_big, up_small, down_big;
+    if (!make_map(&up_big, w_up, int64_t(a.E) * 2 * a.I, a.H, kBigBox) ||
+        !make_map(&up_small, w_up, int64_t(a.E) * 2 * a.I, a.H, kSmallBox) ||
+        !make_map(&down_big, w_down, int64_t(a.E) * a.H, a.I, kBigBox))
         return MOE_ERR_CUDA;
-    const int64_t experts = min64(a.E, T * a.k);
-    const auto blocks = [&](int64_t items) { return unsigned(min64(items, a.spread)); };
     const bool fp8 = a.x_scales != nullptr;
     const auto up = fp8 ? layer_kernel<true, true> : layer_kernel<true, false>;
     const auto down = layer_kernel<false, true>;
-    a.stages = ring_stages(a, fp8);
-    size_t smem = smem_bytes(a, fp8);
-    if (!opt_in_smem((const void*)up, int(smem))) return MOE_ERR_CUDA;
-    up<<<blocks(experts * (a.I / kUpCols)), kThreads, smem, s>>>(m_up, a);
+    if (!opt_in_smem((const void*)up, kSmemBytes) || !opt_in_smem((const void*)down, kSmemBytes))
+        return MOE_ERR_CUDA;
+    // two accumulators of as many columns as a B tile has rows, a power of two
+    const auto cols = [&](bool two) { return (T <= 16 ? 32u : T <= 32 ? 64u : 128u) << (two ? 1 : 0); };
+    a.tmem_cols = cols(fp8);
+    up<<<unsigned(a.spread), kThreads, kSmemBytes, s>>>(up_big, up_small, a);
     if (launch_status() != MOE_OK) return MOE_ERR_CUDA;
-    a.stages = ring_stages(a, true);
-    smem = smem_bytes(a, true);
-    if (!opt_in_smem((const void*)down, int(smem))) return MOE_ERR_CUDA;
-    return launch_dependent(down, unsigned(a.spread), kThreads, smem, s, m_down, a) == cudaSuccess
-               ? MOE_OK : MOE_ERR_CUDA;
+    a.tmem_cols = cols(true);
+    if (launch_dependent(down, unsigned(a.spread), kThreads, kSmemBytes, s, down_big, down_big,
+                         a) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((a.H + 4 * kSumThreads - 1) / (4 * kSumThreads)), unsigned(T));
+    cfg.blockDim = dim3(kSumThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, layer_sum_kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
