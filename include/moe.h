@@ -525,12 +525,13 @@ moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const 
 
 /* ---------------------------------------------- whole layer for few tokens
  * Route, expert FFN and combine of up to MOE_LAYER_DECODE_MAX_TOKENS tokens
- * (a decode step) from the same packed weights as
+ * (a decode step) in one launch (cooperative: a block on every SM, up to 160
+ * of them, at the same time), from the same packed weights as
  * moe_grouped_swiglu ([MOE-OPS] §3, §8, §16; [COMBINE] §1):
  *   out[t] = sum_{j=0..k-1} topk_w[t,j] * y(t, topk_idx[t,j])
  *   y(t,e) = (silu(x_t @ w_gate[e]) * (x_t @ w_up[e])) @ w_down[e]
  * Products are summed in float32, the hidden activation keeps at least 16
- * bits, slots are added in slot order and out [T,H] bf16 is rounded once.  The
+ * bits, slots are added in a fixed order and out [T,H] bf16 is rounded once.  The
  * same inputs give the same bits on every call.
  *
  * moe_layer_decode chooses as moe_route does (the k largest logits, ties to

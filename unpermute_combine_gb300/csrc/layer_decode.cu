@@ -1,36 +1,47 @@
 // layer_decode.cu -- moe_layer_decode, moe_layer_decode_indices: a whole MoE
-// layer for a few tokens.
+// layer for a few tokens, in one launch.
 //
 //   out[t] = sum_j p[t,j] * (silu(x_t Wg[e]^T) * (x_t Wu[e]^T)) Wd[e]^T,  e = idx[t,j]
 //
 // With up to 64 tokens a layer is bound by reading the weights of the experts
-// that some token chose, once: 6 H I bytes each.  Two kernels stream them, the
-// up projections and then the down projections, through the tensor cores with
-// the operands swapped: up to 128 weight rows are the A tile (M = 128) and a
-// group of up to 64 tokens of one expert the B tile (N), so nothing that is read
-// is padding, and the weights go from TMA to shared memory to tcgen05.mma
-// without passing a register.  A third, small kernel adds a token's slots up.
-//   warp 0       TMA producer: stages of weight rows x 64 or 128 of K, in a ring
-//                that fills half of the SM's shared memory, so that two blocks
-//                of either kernel fit an SM
-//   warp 1       one thread issues the MMAs
-//   warps 2..5   fill the B tiles: gathered token rows (e4m3 codes times their
-//                scale) or hidden rows, one warp a stage, so that the latency of
-//                four gathers overlaps (warp 2 also allocates the tensor memory)
-//   warps 6..9   epilogue: silu(gate) * up, or the down products
+// that some token chose, once: 6 H I bytes each.  One block on every SM streams
+// them, first the up projections and then the down projections, through the
+// tensor cores with the operands swapped: up to 128 weight rows are the A tile
+// (M = 128) and a group of up to 64 tokens of one expert the B tile (N), so
+// nothing that is read is padding, and the weights go from TMA to shared memory
+// to tcgen05.mma without passing a register.
+//   warp 0        TMA producer: stages of weight rows x up to 256 of K, in a
+//                 ring that fills the SM's shared memory
+//   warp 1        one thread issues the MMAs
+//   warps 2..10   fill the B tiles: gathered token rows (e4m3 codes times their
+//                 scale) or hidden rows, one warp a stage, so that the latency
+//                 of several gathers overlaps (warp 2 also has the tensor memory)
+//   warp 11       waits for the other blocks
+//   warps 12..15  epilogue: silu(gate) * up, or the down products
 // Precision: the MMA's operands are bf16, but a hidden value, and an e4m3 code
 // times its scale, are not bf16 values.  Both are split into a bf16 value and
 // the bf16 value of the rest (16 bits together), which stand side by side as
 // columns of one B tile; the epilogue adds the two columns.  An MMA this narrow
-// takes as long as its A tile, so the second part costs next to nothing.
-// The second kernel is launched to overlap the first (programmatic dependent
-// launch): its blocks take the place of blocks that finish, and stream the down
-// projections, which do not depend on the first kernel, until their rings are
-// full; only then do they wait for it.
+// takes as long as its A tile (58 cycles measured, a third of the time that the
+// tile takes to arrive), so the second part costs next to nothing.
+// The blocks meet twice (a cooperative launch, so that all of them are
+// resident): before the hidden rows are read, and before the down products of a
+// token's choices are added up.  The weights do not depend on the hidden rows,
+// so a block's ring fills with down projections while it waits.
 // Every block works the routing out for itself (top-k, softmax, each expert's
-// tokens) in shared memory: 64 tokens are too few for a launch of their own.
-// Every wait on an mbarrier is bounded; one that gives up records
-// MOE_ERR_TIMEOUT in the workspace status word.
+// tokens) in shared memory: a launch of its own would take longer.
+// Measured (one call after another in a CUDA graph, other weights each time): one
+// token, 6 of 64 experts, H = 2048, I = 1408: 35 us, of which 11 + 5 stream the
+// weights; the rest is latency (routing 5 us, the two meetings, the last sum).
+// 16 tokens of these: 132 us, 6.2 TB/s; 64 tokens over 256 experts, H = 7168,
+// I = 2048: 2.83 ms, 6.9 TB/s (a copy on the same GPU: 6.7).  Three launches, with
+// the down projections' overlapping the up projections' (35, 139 us and 2.82 ms),
+// did as well for one token and worse in between: each launch worked the routing
+// out anew.  Dot products by warps, without tensor cores: 82 us, 439 us, 12.2 ms.
+// Every wait is bounded; one that gives up records MOE_ERR_TIMEOUT in the
+// workspace status word.
+#include <atomic>
+
 #include "tensor_core.cuh"
 
 namespace moe {
@@ -40,13 +51,24 @@ constexpr int kMaxTokens = 64;
 constexpr int kM = 128;                   // rows of an MMA, weight rows of a down tile
 constexpr int kBigBox = 64, kSmallBox = 16;    // weight rows of a TMA box
 constexpr int kMaxStages = 16;
-constexpr int kLoaders = 4;               // warps that fill B tiles
-constexpr int kThreads = 320;
+constexpr int kLoaders = 9;               // warps that fill B tiles
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kEpilogue = 3 + kLoaders;   // its first warp
+static_assert(kEpilogue + 4 == kWarps && kEpilogue % 4 == 0, "warp roles");
+constexpr int kFly = 8;                   // chunks that a loader's lane has in flight
 constexpr int kExchBytes = 8 * 64 * 4;    // up values on their way to the gate's threads
-constexpr int kBlocksPerSm = 2;
-constexpr int kSmemBytes = 111 * 1024;    // dynamic shared memory of a block, two on an SM
-constexpr int kMaxParts = 8;              // splits of the down projections' K
-constexpr int kSumThreads = 128;
+constexpr int kSmemBytes = 224 * 1024;    // dynamic shared memory of a block, one on an SM
+constexpr int kMaxParts = 8;              // parts of a down tile's K
+constexpr uint32_t kTmemCols = 256;       // two accumulators of up to 128 columns
+// Most blocks of a launch, whatever the GPU.
+constexpr int kMaxBlocks = 160;
+
+// What the blocks meet by, at the same place of every workspace.
+struct Meeting {
+    uint64_t epoch;                       // whatever the last call left
+    uint64_t pad[31];
+    uint64_t flag[2][kMaxBlocks];         // a block sets its own to the call's token
+};
 
 struct LayerArgs {
     const void* x;              // bf16 [T,H], or e4m3 codes
@@ -58,14 +80,13 @@ struct LayerArgs {
     float* topk_w;
     uint16_t* out;              // [T,H] bf16
     WsHeader* header;
-    int* slots;                 // [2 + T*k]: units, slots in use, slot of each choice
-    float* weights;             // [T*k]
+    Meeting* meeting;
+    uint64_t nonce;             // another one for each call from the host
     uint16_t* hidden;           // [2][T*k, I] bf16: the values, and what they leave
-    float* y;                   // [parts][slots, H]
+    float* y;                   // [T*k, H], a row for each choice
+    float* parts;               // [2 * kMaxBlocks][min(group, T)][kM]: the tiles that are cut
     int T, E, k;
-    int64_t H, I;
-    int spread;                 // blocks that fit the GPU at once
-    uint32_t tmem_cols;
+    int H, I;
 };
 
 // ----------------------------------------------------------------- routing
@@ -75,18 +96,21 @@ struct LayerArgs {
 // group of an expert's tokens that share a B tile.
 struct Routing {
     float* w;                   // [T*k]
-    unsigned long long* mask;   // [E] tokens of each expert
-    int16_t* slot;              // [T*k] slot of a choice, -1 = empty
+    uint32_t* mask;             // [E][2] tokens of each expert, a bit each
+    int16_t* expert;            // [T*k] expert of a choice, -1 = empty
     uint16_t* first;            // [E] first slot of each expert
+    uint16_t* units;            // [E] its first unit
     uint16_t* unit;             // [T*k] expert of each unit
     uint8_t* group;             // [T*k] which group of the expert's tokens it is
     uint8_t* token;             // [T*k] token of each slot
-    int* count;                 // [4]: units, bad choices, slots, tokens of a group
+    uint16_t* choice;           // [T*k] t*k + j of each slot
+    int* count;                 // [4]: units, bad choices, tokens of a group
+    int* sums;                  // [3 * kWarps] a warp's sums over its experts
 };
 
 __host__ __device__ inline size_t routing_bytes(int T, int E, int k) {
     const size_t n = size_t(T) * k;
-    const size_t b = 16 + size_t(E) * 8 + n * 4 + n * 2 + size_t(E) * 2 + n * 2 + n + n;
+    const size_t b = 16 + 12 * kWarps + size_t(E) * 12 + n * 12;
     return (b + 127) / 128 * 128;
 }
 
@@ -94,14 +118,27 @@ __device__ __forceinline__ Routing carve_routing(uint8_t* p, int T, int E, int k
     const int n = T * k;
     Routing r;
     r.count = reinterpret_cast<int*>(p);
-    r.mask = reinterpret_cast<unsigned long long*>(p + 16);
-    r.w = reinterpret_cast<float*>(r.mask + E);
-    r.slot = reinterpret_cast<int16_t*>(r.w + n);
-    r.first = reinterpret_cast<uint16_t*>(r.slot + n);
-    r.unit = r.first + E;
-    r.group = reinterpret_cast<uint8_t*>(r.unit + n);
+    r.sums = r.count + 4;
+    r.mask = reinterpret_cast<uint32_t*>(r.sums + 3 * kWarps);
+    r.w = reinterpret_cast<float*>(r.mask + 2 * E);
+    r.expert = reinterpret_cast<int16_t*>(r.w + n);
+    r.first = reinterpret_cast<uint16_t*>(r.expert + n);
+    r.units = r.first + E;
+    r.unit = r.units + E;
+    r.choice = r.unit + n;
+    r.group = reinterpret_cast<uint8_t*>(r.choice + n);
     r.token = r.group + n;
     return r;
+}
+
+// How many tokens expert e has, and how many of them come before token t.
+__device__ __forceinline__ int tokens_of(const Routing& r, int e) {
+    return __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1]);
+}
+__device__ __forceinline__ int tokens_before(const Routing& r, int e, int t) {
+    const uint32_t below = (1u << (t & 31)) - 1u;
+    return t < 32 ? __popc(r.mask[2 * e] & below)
+                  : __popc(r.mask[2 * e]) + __popc(r.mask[2 * e + 1] & below);
 }
 
 // Order-preserving key of a float; -0 is +0, as for a comparison of floats.
@@ -114,65 +151,95 @@ __device__ __forceinline__ float key_logit(uint32_t u) {
     return __uint_as_float(u ^ (uint32_t(int32_t(~u) >> 31) | 0x80000000u));
 }
 
-// The warp's token: its k largest logits, largest first, equal ones by id, and
-// their softmax.  Lane j gets choice j.
-template <int NV>
-__device__ __forceinline__ void top_k(const float* logits, int E, int k, int& id, float& weight) {
-    const int lane = int(lane_id());
-    uint32_t key[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = e < E ? logit_key(logits[e]) : 0u;
-    }
-    uint32_t my_key = 0;
-    id = -1;
-    for (int j = 0; j < k; ++j) {
-        uint32_t best = key[0];
-        int at = 0;
-#pragma unroll
-        for (int i = 1; i < NV; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu,
-                                             best == top ? uint32_t(lane + 32 * at) : 0xFFFFFFFFu);
-        if ((e & 31u) == uint32_t(lane)) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (uint32_t(i) == (e >> 5)) key[i] = 0u;
-        }
-        if (lane == j) { my_key = top; id = e < uint32_t(E) ? int(e) : -1; }
-    }
-    const float v = key_logit(my_key), v0 = __shfl_sync(0xFFFFFFFFu, v, 0);
-    const float p = lane < k ? expf(v - v0) : 0.0f;
-    float sum = p;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    weight = __fdiv_rn(p, sum);
+__device__ __forceinline__ void note_choice(const Routing& r, int t, int i, int id, float w) {
+    r.expert[i] = int16_t(id);
+    r.w[i] = w;
+    if (id >= 0) atomicOr(&r.mask[2 * id + (t >> 5)], 1u << (t & 31));
 }
 
-// All threads of the block; ends with a barrier.  `publish`: writes the choices
-// out.
-__device__ void route(const LayerArgs& a, const Routing& r, bool publish) {
-    const int lane = int(lane_id()), warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int T = a.T, E = a.E, k = a.k, n = T * k;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) r.mask[e] = 0ull;
-    if (threadIdx.x == 0) r.count[1] = 0;
-    __syncthreads();
-    for (int t = warp; t < T; t += warps) {
-        int id = -1;
-        float w = 0.0f;
-        if (a.logits) {
-            const float* lg = a.logits + int64_t(t) * E;
-            if (E <= 64) top_k<2>(lg, E, k, id, w);
-            else if (E <= 256) top_k<8>(lg, E, k, id, w);
-            else top_k<32>(lg, E, k, id, w);
-            if (publish && lane < k) {
-                a.topk_idx[t * k + lane] = id;
-                a.topk_w[t * k + lane] = w;
+// The choices from the logits.  `lanes` lanes a token, 32 / lanes tokens a warp;
+// a lane has the keys of NV consecutive experts (E <= lanes * NV, k <= lanes).
+template <int NV>
+__device__ __forceinline__ void choose(const LayerArgs& a, const Routing& r, int lanes, bool publish) {
+    const int lane = int(lane_id()) & (lanes - 1), base = int(lane_id()) & ~(lanes - 1);
+    const uint32_t group = lanes == 32 ? 0xFFFFFFFFu : (1u << lanes) - 1u;
+    bool clear = false;
+    // whole warps go round, with tokens that do not exist among theirs
+    for (int t0 = 0; t0 < a.T; t0 += kThreads / lanes) {
+        const int t = t0 + threadIdx.x / lanes;
+        uint32_t key[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane * NV + i;
+            key[i] = t < a.T && e < a.E ? logit_key(__ldg(a.logits + int64_t(t) * a.E + e)) : 0u;
+        }
+        if (!clear) { __syncthreads(); clear = true; }     // the masks are
+        if (t0 + int(threadIdx.x & ~31) / lanes >= a.T) continue;
+        uint32_t my_key = 0;
+        int my_id = -1;
+#pragma unroll 1
+        for (int j = 0; j < a.k; ++j) {
+            // the largest key left; 0: taken, or none
+            uint32_t best = key[0];
+            int at = 0;
+#pragma unroll
+            for (int i = 1; i < NV; ++i)
+                if (key[i] > best) { best = key[i]; at = i; }
+            uint32_t top = best;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+                if (o < lanes) top = max(top, v);
             }
-        } else {
-            int bad = 0;
+            // equal ones: the lowest lane has the lowest id
+            const uint32_t have = (__ballot_sync(0xFFFFFFFFu, best == top) >> base) & group;
+            const int from = __ffs(int(have)) - 1;
+            const int e = __shfl_sync(0xFFFFFFFFu, lane * NV + at, base + from);
+            if (lane == from) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (i == at) key[i] = 0u;
+            }
+            if (lane == j) { my_key = top; my_id = e < a.E ? e : -1; }
+        }
+        // lane j has choice j; their softmax
+        const float v = key_logit(my_key), v0 = __shfl_sync(0xFFFFFFFFu, v, base);
+        const float p = lane < a.k ? expf(v - v0) : 0.0f;
+        float sum = p;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float u = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if (o < lanes) sum += u;
+        }
+        const float w = __fdiv_rn(p, sum);
+        if (t < a.T && lane < a.k) {
+            const int i = t * a.k + lane;
+            if (publish) {
+                a.topk_idx[i] = my_id;
+                a.topk_w[i] = w;
+            }
+            note_choice(r, t, i, my_id, w);
+        }
+    }
+    __syncthreads();
+}
+
+// All threads of the block; the caller ends it with a barrier.  `publish`: writes the choices
+// out.
+__device__ __forceinline__ void route(const LayerArgs& a, const Routing& r, bool publish) {
+    const int lane = int(lane_id()), warp = threadIdx.x >> 5;
+    const int T = a.T, E = a.E, k = a.k, n = T * k;
+    for (int e = threadIdx.x; e < 2 * E; e += kThreads) r.mask[e] = 0u;
+    if (threadIdx.x == 0) r.count[1] = 0;
+    if (a.logits) {
+        // a warp a token; 8 lanes where there are more tokens than warps and few experts
+        if (E <= 256) choose<8>(a, r, T > kWarps && E <= 64 && k <= 8 ? 8 : 32, publish);
+        else choose<32>(a, r, 32, publish);
+    } else {
+        __syncthreads();
+        for (int t = warp; t < T; t += kWarps) {
+            int id = -1, bad = 0;
+            float w = 0.0f;
             if (lane < k) {
                 id = a.given_idx[t * k + lane];
                 w = a.given_w[t * k + lane];
@@ -183,151 +250,254 @@ __device__ void route(const LayerArgs& a, const Routing& r, bool publish) {
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id < 0 ? -1 - lane : id);
             if (id >= 0 && (same & ((1u << lane) - 1u))) { id = -1; bad = 1; }
             if (bad) r.count[1] = 1;
+            if (lane < k) note_choice(r, t, t * k + lane, id, w);
         }
-        if (lane < k) {
-            r.slot[t * k + lane] = int16_t(id);      // the expert, until slots are known
-            r.w[t * k + lane] = w;
-            if (id >= 0) atomicOr(&r.mask[id], 1ull << t);
+        __syncthreads();
+    }
+    // Prefix sums over the experts, `mine` of them a thread: tokens, and units of
+    // 8, 16, 32 or 64 tokens.  Two sums to a word; each is at most 2048.
+    const int mine = (E + kThreads - 1) / kThreads, e0 = min(threadIdx.x * mine, E);
+    const int e1 = min(e0 + mine, E);
+    int lo = 0, hi = 0, ex = 0;                            // tokens, by 8; by 16, by 32; by 64
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+        const int c = tokens_of(r, e);
+        lo += c << 16 | (c + 7) / 8;
+        hi += (c + 15) / 16 << 16 | (c + 31) / 32;
+        ex += (c + 63) / 64;
+    }
+    int ilo = lo, ihi = hi, iex = ex;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, ilo, o), u = __shfl_up_sync(0xFFFFFFFFu, ihi, o);
+        const int x = __shfl_up_sync(0xFFFFFFFFu, iex, o);
+        if (lane >= o) { ilo += v; ihi += u; iex += x; }
+    }
+    if (lane == 31) { r.sums[warp] = ilo; r.sums[kWarps + warp] = ihi; r.sums[2 * kWarps + warp] = iex; }
+    __syncthreads();
+    int all_lo = 0, all_hi = 0, act = 0;
+    ilo -= lo;
+    ihi -= hi;
+    iex -= ex;
+#pragma unroll 4
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) { ilo += all_lo; ihi += all_hi; iex += act; }
+        all_lo += r.sums[i];
+        all_hi += r.sums[kWarps + i];
+        act += r.sums[2 * kWarps + i];
+    }
+    // Tokens of a group: a large group keeps its rows' place in every stage and
+    // leaves less of the ring to weights, a small one reads the weights of an
+    // expert with more tokens again, from L2.  8, unless that is a tenth more
+    // reads; then 16 and 32, by the same rule; then 64.
+    const int by8 = all_lo & 0xFFFF, by16 = all_hi >> 16, by32 = all_hi & 0xFFFF;
+    const int g = by8 * 10 <= act * 11 ? 8 : by16 * 10 <= act * 11 ? 16 : by32 * 10 <= act * 11 ? 32 : 64;
+    int slot = ilo >> 16;
+    int unit = g == 8 ? ilo & 0xFFFF : g == 16 ? ihi >> 16 : g == 32 ? ihi & 0xFFFF : iex;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+        const int c = tokens_of(r, e);
+        r.first[e] = uint16_t(slot);
+        r.units[e] = uint16_t(unit);
+        slot += c;
+        for (int q = 0; q * g < c; ++q, ++unit) {
+            r.unit[unit] = uint16_t(e);
+            r.group[unit] = uint8_t(q);
         }
     }
-    __syncthreads();
-    if (warp == 0) {
-        // Tokens of a group: a large group keeps its rows' place in every stage
-        // and leaves less of the ring to weights, a small one reads the weights
-        // of an expert with more tokens again, from L2.  16, unless that is a
-        // tenth more reads; then 32, by the same rule; then 64.
-        int act = 0, by16 = 0, by32 = 0;
-        for (int e = lane; e < E; e += 32) {
-            const int c = __popcll(r.mask[e]);
-            act += c > 0;
-            by16 += (c + 15) / 16;
-            by32 += (c + 31) / 32;
-        }
-        act = __reduce_add_sync(0xFFFFFFFFu, act);
-        by16 = __reduce_add_sync(0xFFFFFFFFu, by16);
-        by32 = __reduce_add_sync(0xFFFFFFFFu, by32);
-        const int g = by16 * 10 <= act * 11 ? 16 : by32 * 10 <= act * 11 ? 32 : 64;
-        int slots = 0, units = 0;
-        for (int base = 0; base < E; base += 32) {
-            const int e = base + lane;
-            const int c = e < E ? __popcll(r.mask[e]) : 0, u = (c + g - 1) / g;
-            int both = c << 16 | u, incl = both;           // at most 2048 of each
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (e < E) r.first[e] = uint16_t(slots + (incl >> 16) - c);
-            for (int i = 0; i < u; ++i) {
-                r.unit[units + (incl & 0xFFFF) - u + i] = uint16_t(e);
-                r.group[units + (incl & 0xFFFF) - u + i] = uint8_t(i);
-            }
-            const int all = __shfl_sync(0xFFFFFFFFu, incl, 31);
-            slots += all >> 16;
-            units += all & 0xFFFF;
-        }
-        if (lane == 0) { r.count[0] = units; r.count[2] = slots; r.count[3] = g; }
+    if (threadIdx.x == kThreads - 1) {
+        r.count[0] = g == 8 ? by8 : g == 16 ? by16 : g == 32 ? by32 : act;
+        r.count[2] = g;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = r.slot[i], t = i / k;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int e = r.expert[i], t = i / k;
         if (e >= 0) {
-            const int slot = r.first[e] + __popcll(r.mask[e] & ((1ull << t) - 1ull));
+            const int slot = r.first[e] + tokens_before(r, e, t);
             r.token[slot] = uint8_t(t);
-            r.slot[i] = int16_t(slot);
+            r.choice[slot] = uint16_t(i);
         }
     }
-    __syncthreads();
 }
+
+// ----------------------------------------------------------------- meeting
+
+// The token that the blocks of this call meet by: the epoch that the last call
+// left in the workspace and the call's own nonce, mixed (the finalizer of
+// Steele, Lea & Flood, "Fast splittable pseudorandom number generators", 2014).
+// The epoch changes with every call, so a replayed graph, whose nonce does not,
+// meets by other tokens than before; the workspace may hold anything, because
+// flags that nobody set equal a 64-bit token by chance only.
+__device__ __forceinline__ uint64_t meeting_token(uint64_t epoch, uint64_t nonce) {
+    uint64_t z = epoch + nonce * 0x9E3779B97F4A7C15ull;
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    return z ^ (z >> 31);
+}
+
+// One thread, after everything that the block wrote (and a barrier of it).
+__device__ __forceinline__ void arrive(const LayerArgs& a, int which, uint64_t token) {
+    asm volatile("fence.acq_rel.gpu;\n st.relaxed.gpu.global.u64 [%0], %1;"
+                 :: "l"(&a.meeting->flag[which][blockIdx.x]), "l"(token) : "memory");
+}
+
+// One warp: waits until every block has arrived; false after kMeetPolls polls
+// (each takes over half a microsecond).
+constexpr int kMeetPolls = 1 << 22;
+
+__device__ __forceinline__ bool wait_for_blocks(const LayerArgs& a, int which, uint64_t token) {
+    const uint64_t* flag = a.meeting->flag[which] + lane_id();
+    bool here = false;
+#pragma unroll 1
+    for (int i = 0; i < kMeetPolls && !here; ++i) {
+        uint64_t v[kMaxBlocks / 32];                       // all on their way at once
+#pragma unroll
+        for (int b = 0; b < kMaxBlocks / 32; ++b)
+            asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v[b]) : "l"(flag + 32 * b) : "memory");
+        here = true;
+#pragma unroll
+        for (int b = 0; b < kMaxBlocks / 32; ++b)
+            here &= v[b] == token || int(lane_id()) + 32 * b >= int(gridDim.x);
+        here = __all_sync(0xFFFFFFFFu, here);
+    }
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    return here;
+}
+
+// One copy of the wait's code for all of the roles.
+__device__ __noinline__ bool bar_wait(uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity); }
 
 // ------------------------------------------------------------------- tiles
 
-// How the routing is cut into work items, the same in every block.
+// How the routing is cut into a phase's work items, the same in every block.  A
+// tile is 64 gate rows and the matching up rows, or 128 rows of Wd, for one
+// unit; the blocks take the items in turn.  The tiles of the last round, which
+// would leave most blocks without work, are cut further, into fewer columns or
+// into parts of K, so that it is a short one.
 struct Work {
-    int units, strips, parts, items;
-    int cols;                   // up: hidden columns of a tile (as many gate and up rows)
-    int rows;                   // weight rows of a tile
-    int group, subs, steps;     // tokens of a B tile; sub-tiles of a stage; stages of K
+    int units, strips;          // tiles: units * strips
+    int whole, items;           // tiles that are one item each; items
+    int cuts;                   // items of each of the other tiles
+    int group;                  // tokens of a B tile
+    int subs, shift, ksubs;     // sub-tiles (64 of K) of a stage, its logarithm; of all K
     int stage_bytes, stages;
+    int a_sub, b_sub;           // bytes of a sub-tile
+    bool two;                   // the B rows come in two bf16 parts
 };
 
-// parts of the down projections' K, so that there is work for every block
-__device__ __forceinline__ int down_parts(const LayerArgs& a, int units) {
-    const int strips = int(a.H / kM), most = int(min64(kMaxParts, a.I / 128));
-    return units > 0 ? max(1, min(most, a.spread / (units * strips))) : 1;
-}
+// Rounds that `items` take.
+__device__ __forceinline__ int rounds(int items) { return (items + int(gridDim.x) - 1) / int(gridDim.x); }
 
-template <bool kUp, bool kB2>
-__device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r, int ring_bytes) {
+__device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r, int ring_bytes, bool up) {
     Work w;
     w.units = r.count[0];
-    w.group = r.count[3];
-    w.parts = kUp ? 1 : down_parts(a, w.units);
-    // narrower up tiles where there are not enough wide ones for every block
-    w.cols = 64;
-    if (kUp)
-        while (w.cols > 16 && w.units * int(a.I / w.cols) * 4 < a.spread * 3) w.cols /= 2;
-    w.rows = kUp ? 2 * w.cols : kM;
-    w.strips = int(kUp ? a.I / w.cols : a.H / kM);
-    w.items = w.units * w.strips * w.parts;
-    // two sub-tiles a stage (256 bytes of a row) where three such stages fit
-    const int sub = (w.rows + w.group * (kB2 ? 2 : 1)) * 128;
-    const int left = ring_bytes - (kM - w.rows) * 128;     // an MMA reads kM rows all the same
-    w.subs = 6 * sub <= left ? 2 : 1;
+    w.group = r.count[2];
+    w.two = !up || a.x_scales;
+    w.strips = up ? a.I / 64 : a.H / kM;
+    const int tiles = w.units * w.strips, rest = tiles % int(gridDim.x);
+    w.whole = tiles - rest;
+    // An item's own cost is taken as 16 of the 64 columns, and as half a step of
+    // 128 of K.  No more than two rounds of parts: that bounds the workspace.
+    const int steps = a.I / 128;
+    int best = 0x7FFFFFFF;
+    w.cuts = 1;
+#pragma unroll 1
+    for (int c = 1; up ? c <= 4 : c <= min(kMaxParts, steps) && c * rest <= 2 * int(gridDim.x); c = up ? 2 * c : c + 1) {
+        const int cost = rounds(rest * c) * (up ? 64 / c + 16 : 2 * ((steps + c - 1) / c) + 1);
+        if (cost < best) { best = cost; w.cuts = c; }
+    }
+    w.items = w.whole + rest * w.cuts;
+    const int rows = up && w.whole == 0 ? kM / w.cuts : kM;    // of the largest item
+    // As much of a row in one stage, 512 bytes, as leaves three stages: rows are
+    // far apart, and memory is slower the shorter the pieces (16 tokens, 64
+    // experts, H = 2048: 154 us with 128 bytes, 135 with 256, 132 with 512).  Large
+    // groups have long gathers instead, one warp a stage, and want many stages
+    // (64 tokens, 8 of 8 experts: 208 us with three stages, 149 with nine).
+    w.a_sub = rows * 128;
+    w.b_sub = w.two ? w.group * 256 : max(w.group, 16) * 128;
+    const int sub = w.a_sub + w.b_sub;
+    const int left = ring_bytes - (kM - rows) * 128;       // an MMA reads kM rows all the same
+    w.shift = w.group > 16 ? 0 : 12 * sub <= left ? 2 : 1;
+    w.subs = 1 << w.shift;
     w.stage_bytes = w.subs * sub;
     w.stages = min(kMaxStages, left / w.stage_bytes);
-    w.steps = int((kUp ? a.H : a.I) / (64 * w.subs));
+    w.ksubs = (up ? a.H : a.I) / 64;
     return w;
 }
 
-// One work item: a tile of weight rows over the stages [k0, k1) of its K.
+// One work item: (part of) a tile over the sub-tiles [k0, k1) of its K.
 struct Item {
     int e, first, n;            // expert, the unit's first slot, its tokens
-    int strip, part, k0, k1;
+    int strip;
+    int cols, col;              // up: hidden columns, the first of them
+    int cut;                    // down: which part among all parts, -1: the whole tile
+    int k0, k1;
 };
 
-// Up: a unit's strips one after the other.  Down: a strip's units and parts.
-template <bool kUp>
-__device__ __forceinline__ Item item_of(const Work& w, const Routing& r, int i) {
+// Up: a unit's strips one after the other.  Down: a strip's units.
+__device__ __forceinline__ Item item_of(const Work& w, const Routing& r, int i, bool up) {
     Item it;
-    const int q = kUp ? i : i / w.parts;
-    it.part = kUp ? 0 : i % w.parts;
-    const int unit = kUp ? q / w.strips : q % w.units;
-    it.strip = kUp ? q % w.strips : q / w.units;
+    int tile = i, cut = 0, cuts = 1;
+    it.cut = -1;
+    if (i >= w.whole) {
+        const int j = i - w.whole;
+        cuts = w.cuts;
+        tile = j / cuts;
+        cut = j - tile * cuts;
+        tile += w.whole;
+        if (cuts > 1) it.cut = j;
+    }
+    int unit;
+    it.k0 = 0;
+    it.k1 = w.ksubs;
+    it.cols = 64;
+    if (up) {
+        unit = tile / w.strips;
+        it.strip = tile - unit * w.strips;
+        it.cols /= cuts;
+        it.col = it.strip * 64 + cut * it.cols;
+    } else {
+        it.strip = tile / w.units;
+        unit = tile - it.strip * w.units;
+        it.k0 = cut * w.ksubs / cuts;
+        it.k1 = (cut + 1) * w.ksubs / cuts;
+        it.col = 0;
+    }
     it.e = r.unit[unit];
     const int at = r.group[unit] * w.group;
     it.first = r.first[it.e] + at;
-    it.n = min(w.group, __popcll(r.mask[it.e]) - at);
-    it.k0 = it.part * w.steps / w.parts;
-    it.k1 = (it.part + 1) * w.steps / w.parts;
+    it.n = min(w.group, tokens_of(r, it.e) - at);
     return it;
 }
 
 // B rows of n tokens: each part of two takes a multiple of 8, one alone of 16,
 // so that N is a multiple of 16.
-template <bool kB2>
-__device__ __forceinline__ int b_rows(int n) { return kB2 ? (n + 7) & ~7 : (n + 15) & ~15; }
+__device__ __forceinline__ int b_rows(int n, bool two) { return two ? (n + 7) & ~7 : (n + 15) & ~15; }
 
 // What a float's bf16 value leaves of it (0 for an infinity, so that it stays one).
 __device__ __forceinline__ float bf16_rest(float v, float hi) {
     return (__float_as_uint(hi) & 0x7F800000u) == 0x7F800000u ? 0.0f : v - hi;
 }
 
-__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+// Chunk c (8 values of K) of a B row in a sub-tile with 128-byte swizzle.
+__device__ __forceinline__ void put_chunk(uint8_t* tile, int row, int c, uint4 v) {
+    *reinterpret_cast<uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4)) = v;
+}
+
+// 8 e4m3 codes times their scale, as bf16 values and what they leave.
+__device__ __forceinline__ void split_codes(uint2 code, float scale, uint4& hi, uint4& lo) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i], b = v[2 * i + 1];
+        float a, b;
+        e4m3x2_to_f32((i < 2 ? code.x : code.y) >> (16 * (i & 1)), a, b);
+        a *= scale;
+        b *= scale;
         h[i] = pack_bf16x2_rn(a, b);
         l[i] = pack_bf16x2_rn(bf16_rest(a, bf16lo_to_f32(h[i])), bf16_rest(b, bf16hi_to_f32(h[i])));
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-// Chunk c (8 values of K) of a B row in a sub-tile with 128-byte swizzle.
-__device__ __forceinline__ void put_chunk(uint8_t* tile, int row, int c, uint4 v) {
-    *reinterpret_cast<uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4)) = v;
 }
 
 __device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -342,310 +512,402 @@ __device__ __forceinline__ bool any_epilogue(bool v) {
     return r != 0;
 }
 
-// kUp: hidden = silu(x Wg^T) * (x Wu^T) of every active expert's tokens;
-// otherwise y = hidden Wd^T.  kB2: the B rows come in two bf16 parts (e4m3 x,
-// or hidden rows).
-template <bool kUp, bool kB2>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-layer_kernel(const __grid_constant__ CUtensorMap map_big,
-             const __grid_constant__ CUtensorMap map_small, const LayerArgs a) {
+// out[t] = sum over the choices of the weighted down products.  `lanes`
+// neighbouring threads have 4 columns of a token, each a share of the choices
+// (and of their parts); the order of the sum depends on `lanes` alone.
+__device__ __forceinline__ void add_up(const LayerArgs& a, const Routing& r, const Work& w, int lanes,
+                                       int i) {
+    constexpr int kMany = 4;                               // loads in flight
+    const int quad = i / lanes, mine = i & (lanes - 1);
+    const int quads = a.H / 4, t = quad / quads, h = (quad - t * quads) * 4;
+    const int cuts = w.items > w.whole ? w.cuts : 1, n = a.k * cuts;
+    const int tile0 = h / kM * w.units, rows = min(w.group, a.T);
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int m0 = mine; m0 < n; m0 += kMany * lanes) {
+        float4 v[kMany];
+        float p[kMany];
+#pragma unroll
+        for (int q = 0; q < kMany; ++q) {
+            const int m = m0 + q * lanes, j = m / cuts, cut = m - j * cuts;
+            v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            p[q] = 0.0f;
+            const int e = m < n ? r.expert[t * a.k + j] : -1;
+            if (e < 0) continue;
+            const int at = tokens_before(r, e, t);         // the token's place in the expert
+            const int tile = tile0 + r.units[e] + at / w.group;
+            const float* y = a.y + int64_t(t * a.k + j) * a.H + h;
+            if (cuts > 1 && tile >= w.whole)
+                y = a.parts + (int64_t((tile - w.whole) * cuts + cut) * rows + at % w.group) * kM + h % kM;
+            else if (cut > 0)
+                continue;
+            v[q] = __ldcg(reinterpret_cast<const float4*>(y));
+            p[q] = r.w[t * a.k + j];
+        }
+#pragma unroll
+        for (int q = 0; q < kMany; ++q) {
+            s.x = fmaf(p[q], v[q].x, s.x);
+            s.y = fmaf(p[q], v[q].y, s.y);
+            s.z = fmaf(p[q], v[q].z, s.z);
+            s.w = fmaf(p[q], v[q].w, s.w);
+        }
+    }
+#pragma unroll 1
+    for (int o = 1; o < lanes; o <<= 1) {
+        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+        s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+        s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, o);
+        s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, o);
+    }
+    if (mine == 0)
+        *reinterpret_cast<uint2*>(a.out + int64_t(t) * a.H + h) =
+            make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_up_small,
+             const __grid_constant__ CUtensorMap map_down, const LayerArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+    // a phase has its own barriers of the ring, and a ring of its own shape
+    __shared__ __align__(8) uint64_t full_a[2][kMaxStages], full_b[2][kMaxStages], empty[2][kMaxStages];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], hidden_there;
     __shared__ uint32_t s_tmem;
+    __shared__ uint64_t s_token;
     __shared__ volatile int s_failed;
+    __shared__ int s_late;
+    __shared__ Work s_work[2];
 
     const int warp = threadIdx.x >> 5, lane = int(lane_id());
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     const int ring_bytes = kSmemBytes - 1024 - kExchBytes - int(routing_bytes(a.T, a.E, a.k));
-    float* exch = reinterpret_cast<float*>(ring + ring_bytes);                 // [8][cols]
+    float* exch = reinterpret_cast<float*>(ring + ring_bytes);                 // [8][64]
     const Routing r = carve_routing(ring + ring_bytes + kExchBytes, a.T, a.E, a.k);
 
-    if (threadIdx.x == 0) {
-        s_failed = 0;
-        for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(smem_addr(&full_a[s]), 1);
-            mbar_init(smem_addr(&full_b[s]), 1);
-            mbar_init(smem_addr(&empty[s]), 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_addr(&acc_full[b]), 1);
-            mbar_init(smem_addr(&acc_empty[b]), 128);
+    // the tokens' rows, on their way to L2 while the routing is worked out
+    if (blockIdx.x * kThreads + threadIdx.x < a.T * (a.H / 128) * (a.x_scales ? 1 : 2))
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(static_cast<const uint8_t*>(a.x) +
+            int64_t(blockIdx.x * kThreads + threadIdx.x) * 128) : "memory");
+    if (threadIdx.x < 2 * kMaxStages) {
+        const int p = threadIdx.x / kMaxStages, s = threadIdx.x % kMaxStages;
+        mbar_init(smem_addr(&full_a[p][s]), 1);
+        mbar_init(smem_addr(&full_b[p][s]), 1);
+        mbar_init(smem_addr(&empty[p][s]), 1);
+        if (s < 2) {
+            mbar_init(smem_addr(p ? &acc_full[s] : &acc_empty[s]), p ? 1 : 128);
+        } else if (threadIdx.x == 2) {
+            mbar_init(smem_addr(&hidden_there), 1);
+            s_failed = 0;
         }
         mbar_fence_init();
-    }
-    if (warp == 2) {
+    } else if (warp == 1) {
+        if (lane == 0) {
+            prefetch_map(&map_up);
+            prefetch_map(&map_up_small);
+            prefetch_map(&map_down);
+        }
+    } else if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     :: "r"(smem_addr(&s_tmem)), "r"(a.tmem_cols) : "memory");
+                     :: "r"(smem_addr(&s_tmem)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (threadIdx.x == 3 * 32) {
+        uint64_t epoch;
+        asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(epoch) : "l"(&a.meeting->epoch) : "memory");
+        s_token = meeting_token(epoch, a.nonce);
     }
     tc_fence_before();
-    route(a, r, kUp && a.logits && blockIdx.x == 0);       // ends with a barrier
+    route(a, r, a.logits && blockIdx.x == 0);
+    if (warp >= kWarps - 2 && lane == 0)                   // two warps that may have no choices
+        s_work[warp & 1] = work_of(a, r, ring_bytes, (warp & 1) == 0);
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const Work w = work_of<kUp, kB2>(a, r, ring_bytes);
-    const int b_sub = w.group * (kB2 ? 2 : 1) * 128, a_sub = w.rows * 128;
-    // every block of this kernel is resident and has its tensor memory
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (kUp && blockIdx.x == 0) {                          // for the sum over slots
-        if (threadIdx.x == 0) {
-            a.header->status = r.count[1] ? MOE_ERR_DEVICE_CHECK : MOE_OK;
-            a.header->detail = 0;
-            a.slots[0] = w.units;
-            a.slots[1] = r.count[2];
-        }
-        for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
-            a.slots[2 + i] = r.slot[i];
-            a.weights[i] = r.w[i];
-        }
+    if (blockIdx.x == 0 && threadIdx.x == kThreads - 1) {
+        a.header->status = r.count[1] ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+        a.header->detail = 0;
     }
 
+    // Every role: the up phase, then the down phase.  Items of a phase go to the
+    // blocks in turn.
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- TMA producer
-            uint32_t it = 0;
-            for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x) {
-                const Item m = item_of<kUp>(w, r, i);
-                // gate rows and the matching up rows (blocks of 128 each), or rows of Wd
-                const int col = m.strip * w.cols;
-                const int row = kUp ? int(m.e * 2 * a.I) + col / 128 * 256 + col % 128
-                                    : int(m.e * a.H) + m.strip * kM;
-                const int row2 = row + (kUp ? 128 : kM / 2), half = w.rows / 2;
-                for (int ks = m.k0; ks < m.k1; ++ks, ++it) {
-                    const int s = it % w.stages;
-                    const uint32_t turn = it / w.stages;
-                    if (!kUp && turn == 1 && s == 0) wait_for_predecessor();   // the ring is full
-                    if (!mbar_wait(smem_addr(&empty[s]), (turn & 1u) ^ 1u)) { s_failed = 1; break; }
-                    const uint32_t bar = smem_addr(&full_a[s]);
-                    mbar_expect_tx(bar, w.subs * a_sub);
-                    for (int u = 0; u < w.subs; ++u) {
-                        const uint32_t dst = smem_addr(ring + s * w.stage_bytes + u * a_sub);
-                        const int c = (ks * w.subs + u) * 64;
-                        if (half == kBigBox) {
-                            tma_load_2d(dst, &map_big, c, row, bar);
-                            tma_load_2d(dst + kBigBox * 128, &map_big, c, row2, bar);
-                        } else {
-                            for (int b = 0; b < half; b += kSmallBox) {
-                                tma_load_2d(dst + b * 128, &map_small, c, row + b, bar);
-                                tma_load_2d(dst + (half + b) * 128, &map_small, c, row2 + b, bar);
+            // weights leave L2 before what every call needs again
+            const uint64_t once = policy_evict_first();
+#pragma unroll 1
+            for (int phase = 0; phase < 2; ++phase) {
+                const bool up = phase == 0;
+                const Work w = s_work[phase];
+                uint32_t it = 0;
+#pragma unroll 1
+                for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x) {
+                    const Item m = item_of(w, r, i, up);
+                    // gate rows and the matching up rows (blocks of 128 each), or rows of Wd
+                    const int row = up ? m.e * 2 * a.I + m.col / 128 * 256 + m.col % 128
+                                       : m.e * a.H + m.strip * kM;
+                    const int row2 = row + (up ? 128 : kM / 2), half = m.cols;
+#pragma unroll 1
+                    for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
+                        const int s = it % w.stages;
+                        if (!bar_wait(smem_addr(&empty[phase][s]), ((it / w.stages) & 1u) ^ 1u)) {
+                            s_failed = 1;
+                            break;
+                        }
+                        const uint32_t bar = smem_addr(&full_a[phase][s]);
+                        const int subs = min(w.subs, m.k1 - k);
+                        mbar_expect_tx(bar, subs * half * 256);
+#pragma unroll 1
+                        for (int u = 0; u < subs; ++u) {
+                            const uint32_t dst = smem_addr(ring + s * w.stage_bytes + u * w.a_sub);
+                            const int c = (k + u) * 64;
+                            const int box = half == kBigBox ? kBigBox : kSmallBox;
+                            const CUtensorMap* map = !up ? &map_down
+                                                     : half == kBigBox ? &map_up : &map_up_small;
+#pragma unroll 1
+                            for (int b = 0; b < half; b += box) {
+                                tma_load_2d_hint(dst + b * 128, map, c, row + b, bar, once);
+                                tma_load_2d_hint(dst + (half + b) * 128, map, c, row2 + b, bar, once);
                             }
                         }
                     }
                 }
+                // The ring takes another shape once its MMAs have read it.  A block
+                // that gave up leaves no copy of its own in flight.
+#pragma unroll 1
+                for (uint32_t b = it > uint32_t(w.stages) ? it - w.stages : 0; b < it; ++b) {
+                    const int s = b % w.stages;
+                    const uint32_t ph = (b / w.stages) & 1u;
+                    if (!s_failed && !bar_wait(smem_addr(&empty[phase][s]), ph)) s_failed = 1;
+                    if (s_failed) bar_wait(smem_addr(&full_a[phase][s]), ph);
+                }
             }
-            // a block that gave up leaves no copy of its own in flight
-            if (s_failed)
-                for (uint32_t b = it > uint32_t(w.stages) ? it - w.stages : 0; b < it; ++b)
-                    mbar_wait(smem_addr(&full_a[b % w.stages]), (b / w.stages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0) {
             // ------------------------------------------------------ MMA issuer
-            if (!kUp) wait_for_predecessor();
-            uint32_t it = 0, tile = 0;
-            for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x, ++tile) {
-                const Item m = item_of<kUp>(w, r, i);
-                const uint32_t idesc = idesc_bf16(kM, b_rows<kB2>(m.n) * (kB2 ? 2 : 1));
-                const uint32_t buf = tile & 1u, acc = tmem + buf * (a.tmem_cols / 2);
-                if (!mbar_wait(smem_addr(&acc_empty[buf]), ((tile >> 1) & 1u) ^ 1u)) { s_failed = 1; break; }
-                tc_fence_after();
-                for (int ks = m.k0; ks < m.k1; ++ks, ++it) {
-                    const int s = it % w.stages;
-                    const uint32_t ph = (it / w.stages) & 1u;
-                    if (!mbar_wait(smem_addr(&full_b[s]), ph) ||
-                        !mbar_wait(smem_addr(&full_a[s]), ph)) { s_failed = 1; break; }
-                    tc_fence_after();
-                    const uint32_t wa = smem_addr(ring + s * w.stage_bytes), xb = wa + w.subs * a_sub;
-                    for (int u = 0; u < w.subs; ++u) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16(acc, smem_desc_k128(wa + u * a_sub + kk * 32),
-                                     smem_desc_k128(xb + u * b_sub + kk * 32), idesc,
-                                     ks != m.k0 || u || kk);
+            uint32_t tile = 0;
+#pragma unroll 1
+            for (int phase = 0; phase < 2; ++phase) {
+                const bool up = phase == 0;
+                const Work w = s_work[phase];
+                uint32_t it = 0;
+#pragma unroll 1
+                for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x, ++tile) {
+                    const Item m = item_of(w, r, i, up);
+                    const uint32_t idesc = idesc_bf16(kM, b_rows(m.n, w.two) * (w.two ? 2 : 1));
+                    const uint32_t buf = tile & 1u, acc = tmem + buf * (kTmemCols / 2);
+                    if (!bar_wait(smem_addr(&acc_empty[buf]), ((tile >> 1) & 1u) ^ 1u)) {
+                        s_failed = 1;
+                        break;
                     }
-                    mma_commit(smem_addr(&empty[s]));
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
+                        const int s = it % w.stages;
+                        const uint32_t ph = (it / w.stages) & 1u;
+                        if (!bar_wait(smem_addr(&full_b[phase][s]), ph) ||
+                            !bar_wait(smem_addr(&full_a[phase][s]), ph)) {
+                            s_failed = 1;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t wa = smem_addr(ring + s * w.stage_bytes);
+#pragma unroll 1
+                        for (int u = 0; u < min(w.subs, m.k1 - k); ++u) {
+                            // along K inside the swizzled row: 16 values, 32 bytes, 2 in the
+                            // descriptor's address
+                            const uint64_t ad = smem_desc_k128(wa + u * w.a_sub);
+                            const uint64_t bd = smem_desc_k128(wa + w.subs * w.a_sub + u * w.b_sub);
+                            mma_bf16(acc, ad, bd, idesc, k != m.k0 || u);
+#pragma unroll
+                            for (int kk = 1; kk < 4; ++kk)
+                                mma_bf16(acc, ad + 2 * kk, bd + 2 * kk, idesc, 1);
+                        }
+                        mma_commit(smem_addr(&empty[phase][s]));
+                    }
+                    if (s_failed) break;
+                    mma_commit(smem_addr(&acc_full[buf]));
                 }
-                if (s_failed) break;
-                mma_commit(smem_addr(&acc_full[buf]));
             }
         }
+    } else if (warp == kEpilogue - 1) {
+        // --------------------------------------------- waits for the other blocks
+        if (!wait_for_blocks(a, 0, s_token)) s_failed = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&hidden_there));
     } else if (warp < 2 + kLoaders) {
         // ----------------------------------------------------------- B loaders
-        if (!kUp) wait_for_predecessor();                  // the hidden rows
-        // No more warps than stages: a warp that waits for a stage has seen the
-        // use before its own last one end, so the stage's barrier can be at most
-        // one phase behind and the parity is not mistaken for an older one.
-        const uint32_t loaders = min(kLoaders, w.stages), mine = warp - 2;
-        const int row_chunks = 8 * w.subs, row_shift = w.subs == 2 ? 4 : 3;
-        uint32_t it = 0;
         bool stop = false;                                 // the same in all lanes
-        for (int i = blockIdx.x; i < w.items && !stop; i += gridDim.x) {
-            const Item m = item_of<kUp>(w, r, i);
-            const int chunks = m.n * row_chunks, part2 = b_rows<kB2>(m.n) * 128;
-            for (int ks = m.k0; ks < m.k1; ++ks, ++it) {
-                if (it % loaders != mine) continue;
-                const int s = it % w.stages;
-                uint8_t* tile = ring + s * w.stage_bytes + w.subs * a_sub;
-                bool ready = false;
-                for (int c0 = 0; c0 < chunks; c0 += 128) {
-                    // up to four chunks a lane in flight; the first ones before the wait
-                    uint4 v[4], v2[4];
-                    float sc[4];
+#pragma unroll 1
+        for (int phase = 0; phase < 2 && !stop; ++phase) {
+            const bool up = phase == 0;
+            const Work w = s_work[phase];
+            // No more warps than stages: a warp that waits for a stage has seen the
+            // use before its own last one end, so the stage's barrier can be at most
+            // one phase behind and the parity is not mistaken for an older one.
+            const uint32_t loaders = min(kLoaders, w.stages), mine = warp - 2;
+            const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
+            uint32_t it = 0;
+            bool met = up;
+#pragma unroll 1
+            for (int i = blockIdx.x; i < w.items && !stop; i += gridDim.x) {
+                const Item m = item_of(w, r, i, up);
+                const int chunks = m.n * row_chunks, part2 = b_rows(m.n, w.two) * 128;
+#pragma unroll 1
+                for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
+                    if (it % loaders != mine) continue;
+                    const int s = it % w.stages;
+                    uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
+                    bool ready = false;
+                    if (!met) {
+                        // every block's hidden rows
+                        if (!bar_wait(smem_addr(&hidden_there), 0)) s_failed = 1;
+                        met = true;
+                    }
+#pragma unroll 1
+                    for (int c0 = 0; c0 < chunks; c0 += 32 * kFly) {
+                        // the first chunks are loaded before the wait
+                        uint4 v[kFly], v2[kFly];
+                        float sc[kFly];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int c = c0 + q * 32 + lane, row = c >> row_shift;
-                        const int col = (ks * row_chunks + (c & (row_chunks - 1))) * 8;
-                        if (c >= chunks) continue;
-                        if (kUp && !kB2) {
-                            v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) +
-                                            r.token[m.first + row] * a.H + col);
-                        } else if (kUp) {
-                            const int t = r.token[m.first + row];
-                            const uint2 code = __ldg(reinterpret_cast<const uint2*>(
-                                static_cast<const uint8_t*>(a.x) + t * a.H + col));
-                            v[q].x = code.x;
-                            v[q].y = code.y;
-                            sc[q] = __ldg(a.x_scales + t * (a.H / 128) + col / 128);
-                        } else {
-                            const uint16_t* p = a.hidden + int64_t(m.first + row) * a.I + col;
-                            v[q] = __ldcg(reinterpret_cast<const uint4*>(p));
-                            v2[q] = __ldcg(reinterpret_cast<const uint4*>(p + int64_t(a.T) * a.k * a.I));
+                        for (int q = 0; q < kFly; ++q) {
+                            const int c = c0 + q * 32 + lane, row = m.first + (c >> row_shift);
+                            const int col = k * 64 + (c & (row_chunks - 1)) * 8;
+                            if (c >= chunks || col >= m.k1 * 64) continue;
+                            if (!up) {
+                                const uint16_t* p = a.hidden + int64_t(row) * a.I + col;
+                                v[q] = __ldcg(reinterpret_cast<const uint4*>(p));
+                                v2[q] = __ldcg(reinterpret_cast<const uint4*>(p + int64_t(a.T) * a.k * a.I));
+                            } else if (!a.x_scales) {
+                                v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) +
+                                                int64_t(r.token[row]) * a.H + col);
+                            } else {
+                                const int t = r.token[row];
+                                const uint2 code = __ldg(reinterpret_cast<const uint2*>(
+                                    static_cast<const uint8_t*>(a.x) + int64_t(t) * a.H + col));
+                                v[q].x = code.x;
+                                v[q].y = code.y;
+                                sc[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
+                            }
+                        }
+                        if (!ready) {
+                            ready = bar_wait(smem_addr(&empty[phase][s]), ((it / w.stages) & 1u) ^ 1u);
+                            if (!ready) { s_failed = 1; break; }
+                        }
+#pragma unroll
+                        for (int q = 0; q < kFly; ++q) {
+                            const int c = c0 + q * 32 + lane, row = c >> row_shift;
+                            const int j = c & (row_chunks - 1);
+                            if (c >= chunks || k * 8 + j >= m.k1 * 8) continue;
+                            if (up && w.two) split_codes(make_uint2(v[q].x, v[q].y), sc[q], v[q], v2[q]);
+                            uint8_t* sub = tile + (j >> 3) * w.b_sub;
+                            put_chunk(sub, row, j & 7, v[q]);
+                            if (w.two) put_chunk(sub + part2, row, j & 7, v2[q]);
                         }
                     }
-                    if (!ready) {
-                        ready = mbar_wait(smem_addr(&empty[s]), ((it / w.stages) & 1u) ^ 1u);
-                        if (!ready) { s_failed = 1; break; }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int c = c0 + q * 32 + lane, row = c >> row_shift;
-                        const int j = c & (row_chunks - 1);
-                        if (c >= chunks) continue;
-                        if (kUp && kB2) {
-                            float f[8];
-                            e4m3x2_to_f32(v[q].x & 0xFFFFu, f[0], f[1]);
-                            e4m3x2_to_f32(v[q].x >> 16, f[2], f[3]);
-                            e4m3x2_to_f32(v[q].y & 0xFFFFu, f[4], f[5]);
-                            e4m3x2_to_f32(v[q].y >> 16, f[6], f[7]);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] *= sc[q];
-                            split8(f, v[q], v2[q]);
-                        }
-                        uint8_t* sub = tile + (j >> 3) * b_sub;
-                        put_chunk(sub, row, j & 7, v[q]);
-                        if (kB2) put_chunk(sub + part2, row, j & 7, v2[q]);
-                    }
+                    // each thread orders its writes before the tensor core's reads
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    stop = __any_sync(0xFFFFFFFFu, s_failed != 0);
+                    if (stop) break;
+                    if (lane == 0) mbar_arrive(smem_addr(&full_b[phase][s]));
                 }
-                // each thread orders its writes before the tensor core's reads
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                stop = __any_sync(0xFFFFFFFFu, s_failed != 0);
-                if (stop) break;
-                if (lane == 0) mbar_arrive(smem_addr(&full_b[s]));
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if (!kUp) wait_for_predecessor();                  // y may still be read
         const int q = warp & 3, row = q * 32 + lane;       // TMEM lane quadrant, tile row
         uint32_t tile = 0;
-        for (int i = blockIdx.x; i < w.items; i += gridDim.x, ++tile) {
-            const Item m = item_of<kUp>(w, r, i);
-            const uint32_t buf = tile & 1u;
-            const uint32_t acc = tmem + buf * (a.tmem_cols / 2) + (uint32_t(q * 32) << 16);
-            const bool ok = !s_failed && mbar_wait(smem_addr(&acc_full[buf]), (tile >> 1) & 1u);
-            // all 128 threads go on, or none
-            if (any_epilogue(!ok)) { s_failed = 1; break; }
-            tc_fence_after();
-            for (int c0 = 0; c0 < m.n; c0 += 8) {
-                float v[8];
-                tmem_ld8(acc + c0, v);
-                if (kB2) {
-                    float lo[8];
-                    tmem_ld8(acc + b_rows<kB2>(m.n) + c0, lo);
+#pragma unroll 1
+        for (int phase = 0; phase < 2; ++phase) {
+            const bool up = phase == 0;
+            const Work w = s_work[phase];
+#pragma unroll 1
+            for (int i = blockIdx.x; i < w.items; i += gridDim.x, ++tile) {
+                const Item m = item_of(w, r, i, up);
+                const uint32_t buf = tile & 1u;
+                const uint32_t acc = tmem + buf * (kTmemCols / 2) + (uint32_t(q * 32) << 16);
+                const bool ok = !s_failed && bar_wait(smem_addr(&acc_full[buf]), (tile >> 1) & 1u);
+                // all 128 threads go on, or none
+                if (any_epilogue(!ok)) { s_failed = 1; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < m.n; c0 += 8) {
+                    float v[8];
+                    tmem_ld8(acc + c0, v);
+                    if (w.two) {
+                        float lo[8];
+                        tmem_ld8(acc + b_rows(m.n, true) + c0, lo);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] += lo[c];
-                }
-                if (kUp) {
-                    // the tile's first rows hold the gate, the next ones the up values
-                    if (row >= w.cols && row < 2 * w.cols) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) exch[c * 64 + row - w.cols] = v[c];
+                        for (int c = 0; c < 8; ++c) v[c] += lo[c];
                     }
-                    bar_epilogue();
-                    if (row < w.cols) {
-                        uint16_t* hp = a.hidden + int64_t(m.first + c0) * a.I + m.strip * w.cols + row;
+                    if (up) {
+                        // the tile's first rows hold the gate, the next ones the up values
+                        if (row >= m.cols && row < 2 * m.cols) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) exch[c * 64 + row - m.cols] = v[c];
+                        }
+                        bar_epilogue();
+                        if (row < m.cols) {
+                            uint16_t* hp = a.hidden + int64_t(m.first + c0) * a.I + m.col + row;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                if (c0 + c >= m.n) break;
+                                const float h = __fdividef(v[c], 1.0f + __expf(-v[c])) *
+                                                exch[c * 64 + row];
+                                const uint16_t hi = f32_to_bf16_rn(h);
+                                hp[int64_t(c) * a.I] = hi;
+                                hp[(int64_t(a.T) * a.k + c) * a.I] =
+                                    f32_to_bf16_rn(bf16_rest(h, bf16_to_f32(hi)));
+                            }
+                        }
+                        bar_epilogue();
+                    } else {
+                        float* yp = a.y + m.strip * kM + row;
+                        float* pp = a.parts + (int64_t(m.cut) * min(w.group, a.T) + c0) * kM + row;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             if (c0 + c >= m.n) break;
-                            const float h = v[c] / (1.0f + expf(-v[c])) * exch[c * 64 + row];
-                            const uint16_t hi = f32_to_bf16_rn(h);
-                            hp[c * a.I] = hi;
-                            hp[(int64_t(a.T) * a.k + c) * a.I] =
-                                f32_to_bf16_rn(bf16_rest(h, bf16_to_f32(hi)));
+                            if (m.cut >= 0) pp[c * kM] = v[c];
+                            else yp[int64_t(r.choice[m.first + c0 + c]) * a.H] = v[c];
                         }
                     }
-                    bar_epilogue();
-                } else {
-                    float* yp = a.y + (int64_t(m.part) * r.count[2] + m.first + c0) * a.H +
-                                m.strip * kM + row;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c0 + c < m.n) yp[c * a.H] = v[c];
                 }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&acc_empty[buf]));
             }
-            tc_fence_before();
-            mbar_arrive(smem_addr(&acc_empty[buf]));
+            // (also where this block gave up: the others go on, and end)
+            bar_epilogue();
+            if (row == 0) arrive(a, phase, s_token);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (s_failed && threadIdx.x == 0) {
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                     :: "r"(tmem), "r"(kTmemCols) : "memory");
+    // the sum over a token's choices, of every block's products
+    // (8 threads share 4 columns while that leaves each at most one of them; the
+    // number of threads is a multiple of a warp's)
+    const int quads = a.T * (a.H / 4), lanes = quads * 8 <= int(gridDim.x) * kThreads ? 8 : 1;
+    if (int(blockIdx.x) * kThreads < quads * lanes) {
+        if (warp == 0) {
+            const bool there = wait_for_blocks(a, 1, s_token);
+            if (lane == 0) s_late = !there;
+        }
+        __syncthreads();
+        if (s_late) s_failed = 1;
+        const Work w = s_work[1];
+#pragma unroll 1
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < quads * lanes; i += gridDim.x * kThreads)
+            add_up(a, r, w, lanes, i);
+    }
+    // every block has met block 0 once: nobody reads this call's epoch any more
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.meeting->epoch = s_token;
+    if (threadIdx.x == 0 && s_failed) {
         a.header->status = MOE_ERR_TIMEOUT;
         a.header->detail = blockIdx.x;
     }
-    __syncwarp();
-    if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
-                     :: "r"(tmem), "r"(a.tmem_cols) : "memory");
-}
-
-// out[t] = sum over the slots, in order, of the weighted down products.  A thread
-// has 4 columns of a token.
-__global__ void __launch_bounds__(kSumThreads) layer_sum_kernel(const LayerArgs a) {
-    __shared__ int s_slot[kMaxTopK];
-    __shared__ float s_w[kMaxTopK];
-    const int t = blockIdx.y;
-    const int64_t h = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 4;
-    wait_for_predecessor();
-    if (int(threadIdx.x) < a.k) {
-        s_slot[threadIdx.x] = __ldcg(a.slots + 2 + t * a.k + threadIdx.x);
-        s_w[threadIdx.x] = __ldcg(a.weights + t * a.k + threadIdx.x);
-    }
-    const int parts = down_parts(a, __ldcg(a.slots));
-    const int64_t part = int64_t(__ldcg(a.slots + 1)) * a.H;
-    __syncthreads();
-    if (h >= a.H) return;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int q = 0; q < parts; ++q) {
-#pragma unroll 8
-        for (int j = 0; j < a.k; ++j) {
-            const int slot = s_slot[j];
-            const float w = s_w[j];
-            // no branch around the load, so that eight of them are in flight
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.y + q * part +
-                                                                    int64_t(max(slot, 0)) * a.H + h));
-            if (slot >= 0) {
-                s.x = fmaf(w, v.x, s.x);
-                s.y = fmaf(w, v.y, s.y);
-                s.z = fmaf(w, v.z, s.z);
-                s.w = fmaf(w, v.w, s.w);
-            }
-        }
-    }
-    *reinterpret_cast<uint2*>(a.out + t * a.H + h) =
-        make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
 }
 
 // -------------------------------------------------------------------- host
@@ -661,29 +923,24 @@ moe_status_t check_layer(int64_t T, int E, int k, int64_t H, int64_t I) {
     return MOE_OK;
 }
 
-// Most blocks that the kernels are launched with, whatever the GPU: a bound of
-// the items that the down projections are split into.
-constexpr int64_t kSpread = 320;
-
-struct Layout { size_t slots, weights, hidden, y, total; };
+struct Layout { size_t meeting, hidden, y, parts, total; };
 
 Layout workspace_layout(int64_t T, int k, int64_t H, int64_t I) {
     const size_t n = size_t(T) * k;
     Layout l;
-    l.slots = kWsAlign;
-    l.weights = l.slots + align_up((2 + n) * 4, kWsAlign);
-    l.hidden = l.weights + align_up(n * 4, kWsAlign);
+    l.meeting = kWsAlign;
+    l.hidden = l.meeting + align_up(sizeof(Meeting), kWsAlign);
     l.y = l.hidden + align_up(n * size_t(I) * 4, kWsAlign);
-    // not split: n rows of H; split: kSpread items of at most T tokens and kM columns
-    l.total = l.y + align_up(max64(int64_t(n) * H, T * kSpread * kM) * 4, kWsAlign);
+    l.parts = l.y + align_up(n * size_t(H) * 4, kWsAlign);
+    l.total = l.parts + align_up(size_t(2 * kMaxBlocks) * T * kM * 4, kWsAlign);
     return l;
 }
 
-moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T, void* workspace,
-                   size_t workspace_bytes, cudaStream_t s) {
-    const moe_status_t st = check_layer(T, a.E, a.k, a.H, a.I);
+moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T, int64_t H,
+                   int64_t I, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+    const moe_status_t st = check_layer(T, a.E, a.k, H, I);
     if (st != MOE_OK) return st;
-    const Layout l = workspace_layout(T, a.k, a.H, a.I);
+    const Layout l = workspace_layout(T, a.k, H, I);
     const bool choices = a.logits ? a.topk_idx && a.topk_w : a.given_idx && a.given_w;
     if (T > 0 && (!a.x || !choices || !w_up || !w_down || !a.out)) return MOE_ERR_INVALID_ARG;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) ||
@@ -698,41 +955,33 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     if (T == 0)
         return cudaMemsetAsync(ws, 0, 8, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     a.T = int(T);
-    a.slots = reinterpret_cast<int*>(ws + l.slots);
-    a.weights = reinterpret_cast<float*>(ws + l.weights);
+    a.H = int(H);
+    a.I = int(I);
+    a.meeting = reinterpret_cast<Meeting*>(ws + l.meeting);
     a.hidden = reinterpret_cast<uint16_t*>(ws + l.hidden);
     a.y = reinterpret_cast<float*>(ws + l.y);
-    a.spread = int(min64(int64_t(sm_count()) * kBlocksPerSm, kSpread));
+    a.parts = reinterpret_cast<float*>(ws + l.parts);
+    static std::atomic<uint64_t> calls{0};
+    a.nonce = calls.fetch_add(1, std::memory_order_relaxed) + 1;
 
-    CUtensorMap up_big, up_small, down_big;
-    if (!make_map(&up_big, w_up, int64_t(a.E) * 2 * a.I, a.H, kBigBox) ||
-        !make_map(&up_small, w_up, int64_t(a.E) * 2 * a.I, a.H, kSmallBox) ||
-        !make_map(&down_big, w_down, int64_t(a.E) * a.H, a.I, kBigBox))
-        return MOE_ERR_CUDA;
-    const bool fp8 = a.x_scales != nullptr;
-    const auto up = fp8 ? layer_kernel<true, true> : layer_kernel<true, false>;
-    const auto down = layer_kernel<false, true>;
-    if (!opt_in_smem((const void*)up, kSmemBytes) || !opt_in_smem((const void*)down, kSmemBytes))
-        return MOE_ERR_CUDA;
-    // two accumulators of as many columns as a B tile has rows, a power of two
-    const auto cols = [&](bool two) { return (T <= 16 ? 32u : T <= 32 ? 64u : 128u) << (two ? 1 : 0); };
-    a.tmem_cols = cols(fp8);
-    up<<<unsigned(a.spread), kThreads, kSmemBytes, s>>>(up_big, up_small, a);
-    if (launch_status() != MOE_OK) return MOE_ERR_CUDA;
-    a.tmem_cols = cols(true);
-    if (launch_dependent(down, unsigned(a.spread), kThreads, kSmemBytes, s, down_big, down_big,
-                         a) != cudaSuccess)
+    CUtensorMap up, up_small, down;
+    if (!make_map(&up, w_up, a.E * 2 * I, H, kBigBox) ||
+        !make_map(&up_small, w_up, a.E * 2 * I, H, kSmallBox) ||
+        !make_map(&down, w_down, a.E * H, I, kBigBox) ||
+        !opt_in_smem((const void*)layer_kernel, kSmemBytes))
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((a.H + 4 * kSumThreads - 1) / (4 * kSumThreads)), unsigned(T));
-    cfg.blockDim = dim3(kSumThreads);
+    cfg.gridDim = dim3(unsigned(min64(sm_count(), kMaxBlocks)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_sum_kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, layer_kernel, up, up_small, down, a) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -765,9 +1014,7 @@ extern "C" moe_status_t moe_layer_decode(const void* x, const float* x_scales, c
     a.out = static_cast<uint16_t*>(out);
     a.E = E;
     a.k = k;
-    a.H = H;
-    a.I = I;
-    return layer(a, w_up_packed, w_down_packed, T, workspace, workspace_bytes,
+    return layer(a, w_up_packed, w_down_packed, T, H, I, workspace, workspace_bytes,
                  static_cast<cudaStream_t>(stream));
 }
 
@@ -787,8 +1034,6 @@ extern "C" moe_status_t moe_layer_decode_indices(const void* x, const float* x_s
     a.out = static_cast<uint16_t*>(out);
     a.E = E;
     a.k = k;
-    a.H = H;
-    a.I = I;
-    return layer(a, w_up_packed, w_down_packed, T, workspace, workspace_bytes,
+    return layer(a, w_up_packed, w_down_packed, T, H, I, workspace, workspace_bytes,
                  static_cast<cudaStream_t>(stream));
 }
