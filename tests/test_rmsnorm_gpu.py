@@ -75,7 +75,8 @@ def _inputs(T, H, dtype, wdtype, residual, seed):
 
 
 SHAPES = [(1, 8), (3, 1), (1, 2048), (5, 7), (33, 136), (2, 1001), (700, 256), (17, 4096),
-          (3, 7168), (2, 8200), (2, 20000), (1, 32768), (1, 40000), (1, 33001)]
+          (3, 7168), (2, 8200), (2, 20000), (1, 32768), (1, 40000), (1, 33001), (400, 2048),
+          (311, 4104), (320, 520), (500, 88), (400, 8184), (330, 130), (3, 8191), (2, 8193)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
@@ -175,7 +176,8 @@ def _e4m3_values(q):
 
 @pytest.mark.parametrize("T,H,block", [(1, 32, 32), (5, 64, 32), (3, 192, 64), (700, 256, 128),
                                        (2, 256, 256), (33, 1280, 256), (4, 7168, 128),
-                                       (2, 8192, 256), (2, 16384, 128), (1, 32768, 64)])
+                                       (2, 8192, 256), (2, 16384, 128), (1, 32768, 64),
+                                       (400, 2048, 128), (333, 96, 32), (310, 8448, 256)])
 @pytest.mark.parametrize("dtype,wdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"),
                                           ("f32", "bf16")])
 @pytest.mark.parametrize("residual", [False, True])
@@ -245,7 +247,8 @@ def _backward64(g, h, w, gh, eps):
 
 
 BWD = [(1, 8), (3, 1), (5, 7), (33, 136), (700, 256), (17, 4096), (2, 1001), (3, 7168), (2, 20000),
-       (1, 33001), (1300, 72), (615, 31)]
+       (1, 33001), (1300, 72), (615, 31), (5, 12000), (900, 512), (3, 8191), (2, 8193), (2500, 24),
+       (400, 2048), (700, 1001)]
 
 
 @pytest.mark.parametrize("T,H", BWD)
