@@ -32,6 +32,11 @@ constexpr int kRingBytes = 200 * 1024;
 
 // ------------------------------------------------------------ loads, stores
 
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float f) { *p = f32_to_bf16_rn(f); }
+__device__ __forceinline__ void store1(float* p, float f) { *p = f; }
+
 // A chunk as it is stored: one 16-byte word of bf16, two of float32.  Rows wait in
 // this form, which takes half the registers of their values.
 template <typename X>
@@ -98,10 +103,52 @@ template <typename X>
 __device__ __forceinline__ void shared8(const X* p, float* f) { values(shared_raw(p), f); }
 template <typename X>
 __device__ __forceinline__ void store8(X* p, const float* f) { store_raw(p, rounded(p, f)); }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ void store1(uint16_t* p, float f) { *p = f32_to_bf16_rn(f); }
-__device__ __forceinline__ void store1(float* p, float f) { *p = f; }
+// Rows that are no multiple of 16 bytes start off a 16-byte boundary, each by its
+// own shift, but all of a call's tensors by the same one.  Their chunks are those
+// of the aligned memory: chunk c has the elements from 8 c - shift on, and the
+// first and the last have some that are another row's.
+template <typename X>
+__device__ __forceinline__ int row_shift(int64_t row, int64_t H) {
+    return int(row * H) & int(16 / sizeof(X) - 1);
+}
+
+// The chunk from element p on, of which those inside [0, H) count (others: 0).
+template <bool kShift, typename X>
+__device__ __forceinline__ Raw<X> load_at(const X* row, int p, int H) {
+    if constexpr (kShift) {
+        if (p < 0 || p + kChunk > H) {
+            float f[kChunk];
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) f[i] = p + i >= 0 && p + i < H ? load1(row + p + i) : 0.0f;
+            return rounded(row, f);
+        }
+    }
+    return load_raw(row + p);
+}
+template <bool kShift, typename X>
+__device__ __forceinline__ void store_at(X* row, int p, int H, const Raw<X>& r) {
+    if constexpr (kShift) {
+        if (p < 0 || p + kChunk > H) {
+            float f[kChunk];
+            values(r, f);
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (p + i >= 0 && p + i < H) store1(row + p + i, f[i]);
+            return;
+        }
+    }
+    store_raw(row + p, r);
+}
+// A chunk of the weight, which the shift moves off its own boundaries.
+template <bool kShift, typename W>
+__device__ __forceinline__ void weight_at(const W* w, int p, int H, float* f) {
+    if constexpr (kShift) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) f[i] = load1(w + min(max(p + i, 0), H - 1));
+    } else {
+        load8(w + p, f);
+    }
+}
 
 // The value as it is stored.
 __device__ __forceinline__ float as_stored(const uint16_t*, float f) {
@@ -114,8 +161,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// four floats -> four e4m3 bytes of f / s.  inv = 1 / s: a product costs a tenth of
-// a division, and is off by a float ulp, where y is by several.
+// four floats -> four e4m3 bytes of f / s, with inv = 1 / s: a product costs a tenth
+// of a division, and is off by two float ulp, where y is by several.
 __device__ __forceinline__ uint32_t q4(const float* f, float inv) {
     return e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
 }
@@ -158,21 +205,23 @@ struct NormArgs {
 
 // A row to blockDim.x threads (a warp, blockDim.y rows a block; or the block), V
 // chunks a thread held in registers between the two passes over the row.
-template <typename X, typename W, int V, bool kQuant>
+template <typename X, typename W, int V, bool kQuant, bool kShift>
 __global__ void __launch_bounds__(V >= 4 ? kMaxThreads / 2 : kMaxThreads)
 rmsnorm_kernel(const NormArgs a) {
     __shared__ float s_part[2][kMaxWarps];
-    const int chunks = int(a.H / kChunk);
+    const int H = int(a.H);
     int turn = 0;
     for (int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y; row < a.T;
          row += int64_t(gridDim.x) * blockDim.y, turn ^= 1) {
         const X* x = static_cast<const X*>(a.x) + row * a.H;
+        const int shift = kShift ? row_shift<X>(row, a.H) : 0;
+        const int chunks = (H + shift + kChunk - 1) / kChunk;
         Raw<X> h[V];
         float ss = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
-            if (c < chunks) h[v] = load_raw(x + c * kChunk);
+            if (c < chunks) h[v] = load_at<kShift>(x, c * kChunk - shift, H);
         }
         if (a.residual) {
             const X* res = static_cast<const X*>(a.residual) + row * a.H;
@@ -181,7 +230,7 @@ rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = threadIdx.x + v * blockDim.x;
-                if (c < chunks) add[v] = load_raw(res + c * kChunk);
+                if (c < chunks) add[v] = load_at<kShift>(res, c * kChunk - shift, H);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -193,7 +242,7 @@ rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) f[i] += g[i];
                     h[v] = rounded(x, f);
-                    store_raw(ho + c * kChunk, h[v]);
+                    store_at<kShift>(ho, c * kChunk - shift, H, h[v]);
                 }
             }
         }
@@ -214,28 +263,31 @@ rmsnorm_kernel(const NormArgs a) {
             float y[kChunk];
             if (c < chunks) {
                 float w[kChunk];
-                load8(static_cast<const W*>(a.weight) + c * kChunk, w);
+                weight_at<kShift>(static_cast<const W*>(a.weight), c * kChunk - shift, H, w);
                 values(h[v], y);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) y[i] = y[i] * r * w[i];
             }
             if (!kQuant) {
-                if (c < chunks) store8(static_cast<X*>(a.out) + row * a.H + c * kChunk, y);
+                if (c < chunks)
+                    store_at<kShift>(static_cast<X*>(a.out) + row * a.H, c * kChunk - shift, H,
+                                     rounded(x, y));
             } else {
-                // the magnitude bits order like the magnitudes; a block's lanes
-                // are consecutive and whole blocks fit a warp (block <= 256)
-                uint32_t m = 0;
+                // a block's lanes are consecutive and whole blocks fit a warp
+                float amax = 0.0f;
                 if (c < chunks) {
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                    for (int i = 0; i < kChunk; ++i) amax = fmaxf(amax, fabsf(y[i]));
                 }
                 for (int o = a.lanes >> 1; o > 0; o >>= 1)
-                    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                const float amax = __uint_as_float(m);
-                const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+                // amax / 448: the product with 1/448, and its remainder put back
+                float s = amax * (1.0f / 448.0f);
+                s = fmaf(fmaf(s, -448.0f, amax), 1.0f / 448.0f, s);
+                if (!(s >= 0x1p-126f)) s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
                 if (c < chunks) {
                     uint2* q = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.H);
-                    const float inv = __frcp_rn(s);
+                    const float inv = __fdividef(1.0f, s);
                     q[c] = s >= 0x1p-126f ? make_uint2(q4(y, inv), q4(y + 4, inv))
                                           : make_uint2(q4_divided(y, s), q4_divided(y + 4, s));
                     if (c % a.lanes == 0) a.scales[row * (chunks / a.lanes) + c / a.lanes] = s;
@@ -245,8 +297,8 @@ rmsnorm_kernel(const NormArgs a) {
     }
 }
 
-// The same for rows that no 16-byte vector fits: elements threadIdx.x, +
-// blockDim.x, ..., eight of them a thread, in registers.
+// The same for tensors that do not start on a 16-byte boundary: elements
+// threadIdx.x, + blockDim.x, ..., eight of them a thread, in registers.
 template <typename X, typename W>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_odd_kernel(const NormArgs a) {
@@ -353,13 +405,20 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* s) {
     return t;
 }
 
+// Bytes of a row's place in the ring.
+template <typename X, bool kShift>
+__host__ __device__ constexpr uint32_t slot_size(int64_t H, bool three) {
+    const int64_t most = kShift ? (H + int64_t(16 / sizeof(X)) - 1 + kChunk - 1) / kChunk * kChunk : H;
+    return uint32_t(most * int64_t(sizeof(X))) * (three ? 3 : 2);
+}
+
 // Rows in teams of blockDim.x threads, blockDim.y teams a block.  A team has a ring
 // of rows in shared memory (h, grad_y and grad_h of each), which bulk copies fill
 // rows ahead, so that reading goes on while a row waits for its sums; V chunks a
 // thread.  The columns' shares of grad_weight stay in registers over all rows of
 // the block; its teams' shares are added up at the end, in order, and the blocks'
 // by rmsnorm_grad_weight_kernel.
-template <typename X, typename W, int V>
+template <typename X, typename W, int V, bool kShift>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -368,9 +427,14 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     __shared__ volatile int s_failed[kMaxTeams];
     const int team = threadIdx.y, teams = blockDim.y, nw = blockDim.x >> 5;
     const int warp = threadIdx.x >> 5;
-    const int chunks = int(a.H / kChunk);
-    const uint32_t row_bytes = uint32_t(a.H) * sizeof(X);
-    const uint32_t slot_bytes = row_bytes * (a.gh ? 3 : 2);
+    const int H = int(a.H);
+    const int64_t first = int64_t(blockIdx.x) * teams + team, step = int64_t(gridDim.x) * teams;
+    // (step is a multiple of 8 where there is a shift: it is the same for all of a
+    // team's rows, and a thread's chunks are the same columns in all of them)
+    const int shift = kShift ? row_shift<X>(first, a.H) : 0;
+    const int chunks = (H + shift + kChunk - 1) / kChunk;
+    const uint32_t slot_bytes = slot_size<X, kShift>(a.H, a.gh != nullptr);
+    const uint32_t row_bytes = slot_bytes / (a.gh ? 3 : 2);
     uint8_t* ring = smem + size_t(team) * a.ring * slot_bytes;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.ring; ++i) mbar_init(smem_addr(&full[team][i]), 1);
@@ -378,34 +442,66 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     }
     if (threadIdx.x == 0) s_failed[team] = 0;
     __syncthreads();
-    const int64_t first = int64_t(blockIdx.x) * teams + team, step = int64_t(gridDim.x) * teams;
     const int64_t rows = first < a.T ? (a.T - first + step - 1) / step : 0;
+    // elements of the team's n-th row, from its shift on, that bulk copies bring: whole
+    // 16-byte words, of which the tensor's last may be cut off
+    constexpr int kWord = int(16 / sizeof(X));
+    auto brought = [&](int64_t n) -> int {
+        if (!kShift) return H;
+        const int64_t at = (first + n * step) * a.H - shift, left = a.T * a.H - at;
+        const int whole = (H + shift + kWord - 1) / kWord * kWord;
+        return left >= whole ? whole : int(left / kWord * kWord);
+    };
     auto fill = [&](int64_t n) {                           // one thread: the team's n-th row
         const int slot = int(n % a.ring);
         const uint32_t bar = smem_addr(&full[team][slot]), dst = smem_addr(ring + slot * slot_bytes);
-        const int64_t at = (first + n * step) * a.H;
-        mbar_expect_tx(bar, slot_bytes);
-        bulk_load(dst, static_cast<const X*>(a.h) + at, row_bytes, bar);
-        bulk_load(dst + row_bytes, static_cast<const X*>(a.g) + at, row_bytes, bar);
-        if (a.gh) bulk_load(dst + 2 * row_bytes, static_cast<const X*>(a.gh) + at, row_bytes, bar);
+        const uint32_t bytes = uint32_t(brought(n)) * uint32_t(sizeof(X));
+        const int64_t at = (first + n * step) * a.H - shift;
+        mbar_expect_tx(bar, bytes * (a.gh ? 3 : 2));
+        if (kShift && bytes == 0) return;
+        bulk_load(dst, static_cast<const X*>(a.h) + at, bytes, bar);
+        bulk_load(dst + row_bytes, static_cast<const X*>(a.g) + at, bytes, bar);
+        if (a.gh) bulk_load(dst + 2 * row_bytes, static_cast<const X*>(a.gh) + at, bytes, bar);
     };
     if (threadIdx.x == 0)
         for (int64_t n = 0; n < rows && n < a.ring; ++n) fill(n);
+    Raw<W> weight[V];
     float dw[V][kChunk] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = threadIdx.x + v * blockDim.x;
+        if (c < chunks) {
+            float f[kChunk];
+            weight_at<kShift>(static_cast<const W*>(a.weight), c * kChunk - shift, H, f);
+            weight[v] = rounded(static_cast<const W*>(a.weight), f);
+        }
+    }
     for (int64_t n = 0; n < rows; ++n) {
         const int slot = int(n % a.ring);
         if (!mbar_wait(smem_addr(&full[team][slot]), uint32_t(n / a.ring) & 1u)) s_failed[team] = 1;
-        const X* h = reinterpret_cast<const X*>(ring + slot * slot_bytes);
-        const X* g = reinterpret_cast<const X*>(ring + slot * slot_bytes + row_bytes);
+        const uint8_t* row = ring + slot * slot_bytes;
+        const int have = brought(n);
+        // chunk c of the row's `which`th tensor
+        auto chunk = [&](int which, const void* tensor, int c, float* f) {
+            shared8(reinterpret_cast<const X*>(row + which * row_bytes) + c * kChunk, f);
+            const int p = c * kChunk - shift;
+            if (!kShift || (p >= 0 && p + kChunk <= H && (c + 1) * kChunk <= have)) return;
+            const X* at = static_cast<const X*>(tensor) + (first + n * step) * a.H + p;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                if (p + i < 0 || p + i >= H) f[i] = 0.0f;
+                else if (c * kChunk + i >= have) f[i] = load1(at + i);
+            }
+        };
         float ss = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
             if (c < chunks) {
                 float hv[kChunk], gv[kChunk], w[kChunk];
-                shared8(h + c * kChunk, hv);
-                shared8(g + c * kChunk, gv);
-                load8(static_cast<const W*>(a.weight) + c * kChunk, w);
+                chunk(0, a.h, c, hv);
+                chunk(1, a.g, c, gv);
+                values(weight[v], w);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
                     ss = fmaf(hv[i], hv[i], ss);
@@ -446,9 +542,9 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
             const int c = threadIdx.x + v * blockDim.x;
             if (c < chunks) {
                 float hv[kChunk], gv[kChunk], w[kChunk], o[kChunk];
-                shared8(h + c * kChunk, hv);
-                shared8(g + c * kChunk, gv);
-                load8(static_cast<const W*>(a.weight) + c * kChunk, w);
+                chunk(0, a.h, c, hv);
+                chunk(1, a.g, c, gv);
+                values(weight[v], w);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
                     dw[v][i] = fmaf(gv[i], hv[i] * r, dw[v][i]);
@@ -456,11 +552,12 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
                 }
                 if (a.gh) {
                     float e[kChunk];
-                    shared8(h + 2 * a.H + c * kChunk, e);
+                    chunk(2, a.gh, c, e);
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) o[i] += e[i];
                 }
-                store8(static_cast<X*>(a.gx) + (first + n * step) * a.H + c * kChunk, o);
+                X* gx = static_cast<X*>(a.gx) + (first + n * step) * a.H;
+                store_at<kShift>(gx, c * kChunk - shift, H, rounded(gx, o));
             }
         }
         // the row has been read by the whole team: its slot takes another
@@ -472,29 +569,30 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     }
     __syncthreads();
     if (threadIdx.x == 0 && s_failed[team]) atomicExch(status, uint32_t(MOE_ERR_TIMEOUT));
-    // the teams' shares one after the other, in the ring's place
+    // the teams' shares one after the other, by columns in the ring's place
     float* sum = reinterpret_cast<float*>(smem);
     for (int t = 0; t < teams; ++t) {
         if (t == team) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int c = threadIdx.x + v * blockDim.x;
+                const int c = threadIdx.x + v * blockDim.x, p = c * kChunk - shift;
                 if (c < chunks) {
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        if (t > 0) dw[v][i] += sum[i * chunks + c];
-                        if (t + 1 < teams) sum[i * chunks + c] = dw[v][i];
-                    }
-                    if (t + 1 == teams) store8(a.partial + int64_t(blockIdx.x) * a.H + c * kChunk, dw[v]);
+                    for (int i = 0; i < kChunk; ++i)
+                        if (!kShift || (p + i >= 0 && p + i < H))
+                            sum[p + i] = t > 0 ? sum[p + i] + dw[v][i] : dw[v][i];
                 }
             }
         }
         __syncthreads();
     }
+    const int threads = blockDim.x * blockDim.y;
+    for (int c = team * blockDim.x + threadIdx.x; c < H; c += threads)
+        a.partial[int64_t(blockIdx.x) * a.H + c] = sum[c];
 }
 
-// Rows that no 16-byte vector fits: elements threadIdx.x, + blockDim.x, ..., eight
-// of them a thread; the next row's are loaded while this one's are worked on.
+// Tensors that do not start on a 16-byte boundary: elements threadIdx.x, +
+// blockDim.x, ..., eight of them a thread; the next row's are loaded while this one's are worked on.
 template <typename X, typename W>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_backward_odd_kernel(const BwdArgs a) {
@@ -613,80 +711,103 @@ int warps_up(int64_t n) { return int((n + 31) / 32 * 32); }
 // The smallest number of chunks a thread whose block fits kMaxThreads; 0: the row
 // does not fit.
 int row_chunks(int64_t H) {
-    if (H / kChunk <= kMaxThreads) return 1;
-    if (H / kChunk <= 2 * kMaxThreads) return 2;
-    return H / kChunk <= 8 * (kMaxThreads / 2) ? 8 : 0;
+    const int64_t chunks = (H + kChunk - 1) / kChunk;
+    if (chunks <= kMaxThreads) return 1;
+    if (chunks <= 2 * kMaxThreads) return 2;
+    return chunks <= 8 * (kMaxThreads / 2) ? 8 : 0;
 }
 
 // Rows of at most kMaxThreads * kChunk elements are held by threads of eight.
 bool odd_fits(int64_t H) { return H <= int64_t(kMaxThreads) * kChunk; }
 
-bool vectors_fit(int64_t H, std::initializer_list<const void*> ptrs) {
-    if (H % kChunk != 0) return false;
+// How a call's rows lie: on 16-byte boundaries, in memory that starts on one, or not.
+enum Rows : int { kVectors, kShifted, kElements };
+
+Rows rows_of(int64_t H, const void* weight, std::initializer_list<const void*> ptrs) {
     for (const void* p : ptrs)
-        if (p && !aligned16(p)) return false;
-    return true;
+        if (p && !aligned16(p)) return kElements;
+    return H % kChunk == 0 && aligned16(weight) ? kVectors : kShifted;
 }
 
 template <typename X, typename W, bool kQuant>
-moe_status_t launch_norm(const NormArgs& a, bool vectors, cudaStream_t s) {
+moe_status_t launch_norm(const NormArgs& a, Rows how, cudaStream_t s) {
     const auto grid = [&](int rows) { return unsigned(min64((a.T + rows - 1) / rows, int64_t(1) << 20)); };
-    if (!vectors && odd_fits(a.H)) {
+    if (how == kElements && odd_fits(a.H)) {
         const int threads = warps_up((a.H + kChunk - 1) / kChunk), rows = threads == 32 ? kWarpRows : 1;
         rmsnorm_odd_kernel<X, W><<<grid(rows), dim3(threads, rows), 0, s>>>(a);
         return launch_status();
     }
-    if (!vectors || row_chunks(a.H) == 0) {
+    const int64_t most = a.H + (how == kShifted ? kChunk : 0);    // with the shift
+    int V = row_chunks(most);
+    if (how == kElements || V == 0) {
         rmsnorm_long_kernel<X, W><<<grid(1), kMaxThreads, 0, s>>>(a);
         return launch_status();
     }
     // Few rows: as many threads a row as it has chunks, which is the shortest way
     // through it.  Many: four chunks a thread, more loads in flight and more rows
-    // an SM (16384 rows of 7168 in bf16: XX us, with one chunk 176).
-    int V = row_chunks(a.H);
-    const int64_t chunks = a.H / kChunk;
-    if (a.T > 2 * sm_count() && chunks > 32) V = chunks > 64 && chunks <= 4 * (kMaxThreads / 2) ? 4 : max64(V, 2);
+    // an SM (16384 rows of 7168 in bf16: 136 us, with two chunks 149, with one 176).
+    const int64_t chunks = (most + kChunk - 1) / kChunk;
+    if (a.T > 2 * sm_count() && chunks > 32) V = int(max64(V, chunks > 64 ? 4 : 2));
     const int threads = warps_up((chunks + V - 1) / V), rows = threads == 32 ? kWarpRows : 1;
     const dim3 block(threads, rows);
-    switch (V) {
-        case 1: rmsnorm_kernel<X, W, 1, kQuant><<<grid(rows), block, 0, s>>>(a); break;
-        case 2: rmsnorm_kernel<X, W, 2, kQuant><<<grid(rows), block, 0, s>>>(a); break;
-        case 4: rmsnorm_kernel<X, W, 4, kQuant><<<grid(rows), block, 0, s>>>(a); break;
-        default: rmsnorm_kernel<X, W, 8, kQuant><<<grid(rows), block, 0, s>>>(a); break;
-    }
+    constexpr bool kMay = !kQuant;                         // e4m3 rows are never shifted
+#define MOE_NORM(v)                                                                              \
+    do {                                                                                         \
+        if (kMay && how == kShifted)                                                             \
+            rmsnorm_kernel<X, W, v, kQuant, kMay><<<grid(rows), block, 0, s>>>(a);               \
+        else                                                                                     \
+            rmsnorm_kernel<X, W, v, kQuant, false><<<grid(rows), block, 0, s>>>(a);              \
+    } while (0)
+    if (V == 1) MOE_NORM(1);
+    else if (V == 2) MOE_NORM(2);
+    else if (V == 4) MOE_NORM(4);
+    else MOE_NORM(8);
+#undef MOE_NORM
     return launch_status();
 }
 
 template <bool kQuant>
-moe_status_t dispatch_norm(const NormArgs& a, int dtype, int wdtype, bool vectors,
+moe_status_t dispatch_norm(const NormArgs& a, int dtype, int wdtype, Rows how,
                            cudaStream_t s) {
     if (dtype == MOE_BF16)
-        return wdtype == MOE_BF16 ? launch_norm<uint16_t, uint16_t, kQuant>(a, vectors, s)
-                                  : launch_norm<uint16_t, float, kQuant>(a, vectors, s);
-    return wdtype == MOE_BF16 ? launch_norm<float, uint16_t, kQuant>(a, vectors, s)
-                              : launch_norm<float, float, kQuant>(a, vectors, s);
+        return wdtype == MOE_BF16 ? launch_norm<uint16_t, uint16_t, kQuant>(a, how, s)
+                                  : launch_norm<uint16_t, float, kQuant>(a, how, s);
+    return wdtype == MOE_BF16 ? launch_norm<float, uint16_t, kQuant>(a, how, s)
+                              : launch_norm<float, float, kQuant>(a, how, s);
+}
+
+template <typename X, typename W, bool kShift>
+moe_status_t launch_ring(BwdArgs a, unsigned* blocks, cudaStream_t s) {
+    const int64_t slot = slot_size<X, kShift>(a.H, a.gh != nullptr);
+    const int64_t chunks = slot / (a.gh ? 3 : 2) / int64_t(kChunk * sizeof(X));
+    const int V = chunks > 32 ? 2 : 1, threads = warps_up((chunks + V - 1) / V);
+    // as many teams as fit (16384 rows of 2048 in bf16: 57 us with 8, 98 with 2, 173
+    // with 1), but no fewer blocks than SMs for them
+    int teams = int(min64(min64(kMaxThreads / threads, kMaxTeams), kRingBytes / (2 * slot)));
+    teams = int(max64(1, min64(teams, (a.T + sm_count() - 1) / sm_count())));
+    a.ring = int(min64(kMaxRing, kRingBytes / (teams * slot)));
+    int64_t most = min64(sm_count(), kBwdMaxBlocks);
+    if (kShift && most >= 8) most -= most % 8;             // the step between a team's rows
+    *blocks = unsigned(min64((a.T + teams - 1) / teams, most));
+    const size_t smem = size_t(max64(int64_t(teams) * a.ring * slot, a.H * 4));
+    const auto kernel = V == 1 ? rmsnorm_backward_kernel<X, W, 1, kShift>
+                               : rmsnorm_backward_kernel<X, W, 2, kShift>;
+    if (!opt_in_smem((const void*)kernel, kRingBytes)) return MOE_ERR_CUDA;
+    uint32_t* status = device_status_word();
+    if (!status) return MOE_ERR_CUDA;
+    kernel<<<*blocks, dim3(threads, teams), smem, s>>>(a, status);
+    return launch_status();
 }
 
 // The backward's blocks (rows of partial sums): the ring has one on every SM, the
 // others as many as help.
 template <typename X, typename W>
-moe_status_t launch_backward(BwdArgs a, bool vectors, unsigned* blocks, cudaStream_t s) {
-    const int64_t slot = a.H * int64_t(sizeof(X)) * (a.gh ? 3 : 2), chunks = a.H / kChunk;
-    if (vectors && 2 * slot <= kRingBytes && chunks <= 2 * kMaxThreads) {
-        const int V = chunks > 32 ? 2 : 1, threads = warps_up((chunks + V - 1) / V);
-        // as many teams as fit, but no fewer blocks than SMs for them
-        int teams = kMaxThreads / threads;
-        teams = int(min64(min64(teams, kMaxTeams), kRingBytes / (2 * slot)));
-        teams = int(max64(1, min64(teams, (a.T + sm_count() - 1) / sm_count())));
-        a.ring = int(min64(kMaxRing, kRingBytes / (teams * slot)));
-        *blocks = unsigned(min64((a.T + teams - 1) / teams, min64(sm_count(), kBwdMaxBlocks)));
-        const size_t smem = size_t(max64(int64_t(teams) * a.ring * slot, a.H * 4));
-        const auto kernel = V == 1 ? rmsnorm_backward_kernel<X, W, 1> : rmsnorm_backward_kernel<X, W, 2>;
-        if (!opt_in_smem((const void*)kernel, kRingBytes)) return MOE_ERR_CUDA;
-        uint32_t* status = device_status_word();
-        if (!status) return MOE_ERR_CUDA;
-        kernel<<<*blocks, dim3(threads, teams), smem, s>>>(a, status);
-        return launch_status();
+moe_status_t launch_backward(const BwdArgs& a, Rows how, unsigned* blocks, cudaStream_t s) {
+    if (how != kElements && 2 * int64_t(slot_size<X, true>(a.H, a.gh != nullptr)) <= kRingBytes &&
+        a.H + kChunk <= 2 * kMaxThreads * kChunk) {
+        if (how == kVectors) return launch_ring<X, W, false>(a, blocks, s);
+        // a shift wants blocks by eights, or no second row for a team
+        if (sm_count() >= 8 || a.T <= sm_count()) return launch_ring<X, W, true>(a, blocks, s);
     }
     *blocks = unsigned(min64(a.T, kBwdMaxBlocks));
     if (odd_fits(a.H))
@@ -721,8 +842,8 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, moe_dty
     if (!x || !weight || !out || (residual && !residual_out)) return MOE_ERR_INVALID_ARG;
     if (!residual) residual_out = nullptr;
     const NormArgs a{x, residual, weight, residual_out, out, nullptr, T, H, eps, 0};
-    const bool vectors = vectors_fit(H, {x, residual, weight, residual_out, out});
-    return dispatch_norm<false>(a, dtype, weight_dtype, vectors, static_cast<cudaStream_t>(stream));
+    const Rows how = rows_of(H, weight, {x, residual, residual_out, out});
+    return dispatch_norm<false>(a, dtype, weight_dtype, how, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status_t moe_rmsnorm_quantize_fp8(const void* x, const void* residual,
@@ -739,11 +860,11 @@ extern "C" moe_status_t moe_rmsnorm_quantize_fp8(const void* x, const void* resi
     if (row_chunks(H) == 0) return MOE_ERR_UNSUPPORTED;
     if (!x || !weight || !x_q || !scales || (residual && !residual_out)) return MOE_ERR_INVALID_ARG;
     if (!residual) residual_out = nullptr;
-    if (!vectors_fit(H, {x, residual, weight, residual_out}) ||
+    if (rows_of(H, weight, {x, residual, residual_out}) != kVectors ||
         (reinterpret_cast<uintptr_t>(x_q) & 7u) || (reinterpret_cast<uintptr_t>(scales) & 3u))
         return MOE_ERR_INVALID_ARG;
     const NormArgs a{x, residual, weight, residual_out, x_q, scales, T, H, eps, block / kChunk};
-    return dispatch_norm<true>(a, dtype, weight_dtype, true, static_cast<cudaStream_t>(stream));
+    return dispatch_norm<true>(a, dtype, weight_dtype, kVectors, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status_t moe_rmsnorm_backward_workspace_size(int64_t T, int64_t H, size_t* bytes) {
@@ -778,14 +899,14 @@ extern "C" moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* gra
         return MOE_ERR_WORKSPACE;
     unsigned blocks = 0;
     const BwdArgs a{grad_y, grad_h, h, weight, grad_x, static_cast<float*>(workspace), T, H, eps, 0};
-    const bool vectors = vectors_fit(H, {grad_y, grad_h, h, weight, grad_x});
+    const Rows how = rows_of(H, weight, {grad_y, grad_h, h, grad_x});
     moe_status_t r;
     if (dtype == MOE_BF16)
-        r = weight_dtype == MOE_BF16 ? launch_backward<uint16_t, uint16_t>(a, vectors, &blocks, s)
-                                     : launch_backward<uint16_t, float>(a, vectors, &blocks, s);
+        r = weight_dtype == MOE_BF16 ? launch_backward<uint16_t, uint16_t>(a, how, &blocks, s)
+                                     : launch_backward<uint16_t, float>(a, how, &blocks, s);
     else
-        r = weight_dtype == MOE_BF16 ? launch_backward<float, uint16_t>(a, vectors, &blocks, s)
-                                     : launch_backward<float, float>(a, vectors, &blocks, s);
+        r = weight_dtype == MOE_BF16 ? launch_backward<float, uint16_t>(a, how, &blocks, s)
+                                     : launch_backward<float, float>(a, how, &blocks, s);
     if (r != MOE_OK) return r;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((H + kSumCols - 1) / kSumCols));
