@@ -112,11 +112,12 @@ __device__ __forceinline__ int row_shift(int64_t row, int64_t H) {
     return int(row * H) & int(16 / sizeof(X) - 1);
 }
 
-// The chunk from element p on, of which those inside [0, H) count (others: 0).
+// The chunk from element p on.  Elements of the rows next to this one come along
+// (clear_others takes them out), but nothing past the tensor's last row is read.
 template <bool kShift, typename X>
-__device__ __forceinline__ Raw<X> load_at(const X* row, int p, int H) {
+__device__ __forceinline__ Raw<X> load_at(const X* row, int p, int H, bool last) {
     if constexpr (kShift) {
-        if (p < 0 || p + kChunk > H) {
+        if (last && p + kChunk > H) {
             float f[kChunk];
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) f[i] = p + i >= 0 && p + i < H ? load1(row + p + i) : 0.0f;
@@ -124,6 +125,16 @@ __device__ __forceinline__ Raw<X> load_at(const X* row, int p, int H) {
         }
     }
     return load_raw(row + p);
+}
+template <bool kShift>
+__device__ __forceinline__ void clear_others(float* f, int p, int H) {
+    if constexpr (kShift) {
+        if (p < 0 || p + kChunk > H) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (p + i < 0 || p + i >= H) f[i] = 0.0f;
+        }
+    }
 }
 template <bool kShift, typename X>
 __device__ __forceinline__ void store_at(X* row, int p, int H, const Raw<X>& r) {
@@ -139,7 +150,8 @@ __device__ __forceinline__ void store_at(X* row, int p, int H, const Raw<X>& r) 
     }
     store_raw(row + p, r);
 }
-// A chunk of the weight, which the shift moves off its own boundaries.
+// A chunk of the weight, which the shift moves off its own boundaries.  (Out of two
+// aligned chunks by selects: no faster.)
 template <bool kShift, typename W>
 __device__ __forceinline__ void weight_at(const W* w, int p, int H, float* f) {
     if constexpr (kShift) {
@@ -204,9 +216,13 @@ struct NormArgs {
 };
 
 // A row to blockDim.x threads (a warp, blockDim.y rows a block; or the block), V
-// chunks a thread held in registers between the two passes over the row.
+// chunks a thread held in registers between the two passes over the row.  Bound
+// by memory: 16384 rows of 7168 in bf16 with a residual take 136 us, 6.9 TB/s (a
+// copy: 6.7); with e4m3 output 153 us, 5.3 TB/s, where the instructions of the
+// quantization fill 60% of the issue slots; rows of 7001 elements 150 us.  64
+// registers where a thread has 64 bytes: with 76, the e4m3 form took 176 us.
 template <typename X, typename W, int V, bool kQuant, bool kShift>
-__global__ void __launch_bounds__(V >= 4 ? kMaxThreads / 2 : kMaxThreads)
+__global__ void __launch_bounds__(V >= 4 ? kMaxThreads / 2 : kMaxThreads, V == 4 ? 2 : 1)
 rmsnorm_kernel(const NormArgs a) {
     __shared__ float s_part[2][kMaxWarps];
     const int H = int(a.H);
@@ -221,7 +237,7 @@ rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
-            if (c < chunks) h[v] = load_at<kShift>(x, c * kChunk - shift, H);
+            if (c < chunks) h[v] = load_at<kShift>(x, c * kChunk - shift, H, row == a.T - 1);
         }
         if (a.residual) {
             const X* res = static_cast<const X*>(a.residual) + row * a.H;
@@ -230,7 +246,7 @@ rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = threadIdx.x + v * blockDim.x;
-                if (c < chunks) add[v] = load_at<kShift>(res, c * kChunk - shift, H);
+                if (c < chunks) add[v] = load_at<kShift>(res, c * kChunk - shift, H, row == a.T - 1);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -252,6 +268,7 @@ rmsnorm_kernel(const NormArgs a) {
             if (c < chunks) {
                 float f[kChunk];
                 values(h[v], f);
+                clear_others<kShift>(f, c * kChunk - shift, H);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) ss = fmaf(f[i], f[i], ss);
             }
@@ -479,19 +496,33 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     for (int64_t n = 0; n < rows; ++n) {
         const int slot = int(n % a.ring);
         if (!mbar_wait(smem_addr(&full[team][slot]), uint32_t(n / a.ring) & 1u)) s_failed[team] = 1;
-        const uint8_t* row = ring + slot * slot_bytes;
-        const int have = brought(n);
-        // chunk c of the row's `which`th tensor
-        auto chunk = [&](int which, const void* tensor, int c, float* f) {
-            shared8(reinterpret_cast<const X*>(row + which * row_bytes) + c * kChunk, f);
-            const int p = c * kChunk - shift;
-            if (!kShift || (p >= 0 && p + kChunk <= H && (c + 1) * kChunk <= have)) return;
-            const X* at = static_cast<const X*>(tensor) + (first + n * step) * a.H + p;
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                if (p + i < 0 || p + i >= H) f[i] = 0.0f;
-                else if (c * kChunk + i >= have) f[i] = load1(at + i);
+        uint8_t* row = ring + slot * slot_bytes;
+        if constexpr (kShift) {
+            // The first and the last chunk are put right in place, once: other rows'
+            // elements become 0, and what no copy brings is loaded.  (In registers,
+            // at each reading: 350 us instead of 189 for 16384 rows of 7172.)
+            if (threadIdx.x < 2 * kChunk) {
+                const int i = (threadIdx.x < kChunk ? 0 : chunks - 1) * kChunk +
+                              int(threadIdx.x & (kChunk - 1));
+                const bool inside = i >= shift && i < H + shift;
+                if (!inside || i >= brought(n)) {
+                    const int64_t at = (first + n * step) * a.H + i - shift;
+                    X* edge = reinterpret_cast<X*>(row) + i;
+                    const int pitch = int(row_bytes / sizeof(X));
+                    edge[0] = inside ? static_cast<const X*>(a.h)[at] : X(0);
+                    edge[pitch] = inside ? static_cast<const X*>(a.g)[at] : X(0);
+                    if (a.gh) edge[2 * pitch] = inside ? static_cast<const X*>(a.gh)[at] : X(0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy
+                }
             }
+            if (nw > 1)
+                asm volatile("bar.sync %0, %1;" :: "r"(team + 1), "r"(blockDim.x) : "memory");
+            else
+                __syncwarp();
+        }
+        // chunk c of the row's `which`th tensor
+        auto chunk = [&](int which, int c, float* f) {
+            shared8(reinterpret_cast<const X*>(row + which * row_bytes) + c * kChunk, f);
         };
         float ss = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -499,8 +530,8 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
             const int c = threadIdx.x + v * blockDim.x;
             if (c < chunks) {
                 float hv[kChunk], gv[kChunk], w[kChunk];
-                chunk(0, a.h, c, hv);
-                chunk(1, a.g, c, gv);
+                chunk(0, c, hv);
+                chunk(1, c, gv);
                 values(weight[v], w);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
@@ -542,8 +573,8 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
             const int c = threadIdx.x + v * blockDim.x;
             if (c < chunks) {
                 float hv[kChunk], gv[kChunk], w[kChunk], o[kChunk];
-                chunk(0, a.h, c, hv);
-                chunk(1, a.g, c, gv);
+                chunk(0, c, hv);
+                chunk(1, c, gv);
                 values(weight[v], w);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
@@ -552,7 +583,7 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
                 }
                 if (a.gh) {
                     float e[kChunk];
-                    chunk(2, a.gh, c, e);
+                    chunk(2, c, e);
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) o[i] += e[i];
                 }
@@ -744,10 +775,11 @@ moe_status_t launch_norm(const NormArgs& a, Rows how, cudaStream_t s) {
         return launch_status();
     }
     // Few rows: as many threads a row as it has chunks, which is the shortest way
-    // through it.  Many: four chunks a thread, more loads in flight and more rows
-    // an SM (16384 rows of 7168 in bf16: 136 us, with two chunks 149, with one 176).
+    // through it.  Many: 64 bytes a thread, more loads in flight and more rows an SM
+    // (16384 rows of 7168 in bf16: 136 us, with 32 bytes 149, with 16 176).
     const int64_t chunks = (most + kChunk - 1) / kChunk;
-    if (a.T > 2 * sm_count() && chunks > 32) V = int(max64(V, chunks > 64 ? 4 : 2));
+    constexpr int kWide = sizeof(X) == 2 ? 4 : 2;
+    if (a.T > 2 * sm_count() && chunks > 32) V = int(max64(V, chunks > 64 ? kWide : 2));
     const int threads = warps_up((chunks + V - 1) / V), rows = threads == 32 ? kWarpRows : 1;
     const dim3 block(threads, rows);
     constexpr bool kMay = !kQuant;                         // e4m3 rows are never shifted
@@ -760,7 +792,7 @@ moe_status_t launch_norm(const NormArgs& a, Rows how, cudaStream_t s) {
     } while (0)
     if (V == 1) MOE_NORM(1);
     else if (V == 2) MOE_NORM(2);
-    else if (V == 4) MOE_NORM(4);
+    else if (V == kWide) MOE_NORM(kWide);
     else MOE_NORM(8);
 #undef MOE_NORM
     return launch_status();
@@ -780,7 +812,8 @@ template <typename X, typename W, bool kShift>
 moe_status_t launch_ring(BwdArgs a, unsigned* blocks, cudaStream_t s) {
     const int64_t slot = slot_size<X, kShift>(a.H, a.gh != nullptr);
     const int64_t chunks = slot / (a.gh ? 3 : 2) / int64_t(kChunk * sizeof(X));
-    const int V = chunks > 32 ? 2 : 1, threads = warps_up((chunks + V - 1) / V);
+    const int V = chunks > 32 ? 2 : 1;
+    const int threads = warps_up((chunks + V - 1) / V);
     // as many teams as fit (16384 rows of 2048 in bf16: 57 us with 8, 98 with 2, 173
     // with 1), but no fewer blocks than SMs for them
     int teams = int(min64(min64(kMaxThreads / threads, kMaxTeams), kRingBytes / (2 * slot)));
