@@ -600,26 +600,24 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     }
     __syncthreads();
     if (threadIdx.x == 0 && s_failed[team]) atomicExch(status, uint32_t(MOE_ERR_TIMEOUT));
-    // the teams' shares one after the other, by columns in the ring's place
-    float* sum = reinterpret_cast<float*>(smem);
-    for (int t = 0; t < teams; ++t) {
-        if (t == team) {
+    // the teams' shares side by side in the ring's place (4 H bytes each, and a ring
+    // has at least 8 H for a team), then a column's sum over the teams, in order
+    float* share = reinterpret_cast<float*>(smem);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = threadIdx.x + v * blockDim.x, p = c * kChunk - shift;
-                if (c < chunks) {
+    for (int v = 0; v < V; ++v) {
+        const int c = threadIdx.x + v * blockDim.x, p = c * kChunk - shift;
+        if (c >= chunks) continue;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i)
-                        if (!kShift || (p + i >= 0 && p + i < H))
-                            sum[p + i] = t > 0 ? sum[p + i] + dw[v][i] : dw[v][i];
-                }
-            }
-        }
-        __syncthreads();
+        for (int i = 0; i < kChunk; ++i)
+            if (!kShift || (p + i >= 0 && p + i < H)) share[team * H + p + i] = dw[v][i];
     }
+    __syncthreads();
     const int threads = blockDim.x * blockDim.y;
-    for (int c = team * blockDim.x + threadIdx.x; c < H; c += threads)
-        a.partial[int64_t(blockIdx.x) * a.H + c] = sum[c];
+    for (int c = team * blockDim.x + threadIdx.x; c < H; c += threads) {
+        float sum = share[c];
+        for (int t = 1; t < teams; ++t) sum += share[t * H + c];
+        a.partial[int64_t(blockIdx.x) * a.H + c] = sum;
+    }
 }
 
 // Tensors that do not start on a 16-byte boundary: elements threadIdx.x, +
@@ -822,7 +820,7 @@ moe_status_t launch_ring(BwdArgs a, unsigned* blocks, cudaStream_t s) {
     int64_t most = min64(sm_count(), kBwdMaxBlocks);
     if (kShift && most >= 8) most -= most % 8;             // the step between a team's rows
     *blocks = unsigned(min64((a.T + teams - 1) / teams, most));
-    const size_t smem = size_t(max64(int64_t(teams) * a.ring * slot, a.H * 4));
+    const size_t smem = size_t(teams) * a.ring * slot;
     const auto kernel = V == 1 ? rmsnorm_backward_kernel<X, W, 1, kShift>
                                : rmsnorm_backward_kernel<X, W, 2, kShift>;
     if (!opt_in_smem((const void*)kernel, kRingBytes)) return MOE_ERR_CUDA;
