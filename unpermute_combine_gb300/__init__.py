@@ -70,6 +70,8 @@ def library_path() -> str:
 def load_library():
     """Load libmoe.so (built in-tree by unpermute_combine_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -195,46 +197,57 @@ def _workspace(nbytes, like, given):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=like.device)
 
 
-class _Target:
-    """Where a call runs: checks that every tensor lies on the current device,
-    and allocates outputs and workspaces for the stream that the kernels run
-    on (a tensor of another stream's pool could still be in use there)."""
+# The norms and the decode layer are called for single tokens, where the time on
+# the host counts: their checks and allocations are kept to what torch does
+# fastest, and pointers are passed as integers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-    def __init__(self, stream, like):
-        self.device = like.device
-        if self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {self.device}, but the current device is "
+
+class _Target:
+    """Where a call runs: the current device, on which every tensor has to lie,
+    and the stream, for which outputs and workspaces are allocated (a tensor of
+    another stream's pool could still be in use there)."""
+
+    __slots__ = ("device", "stream", "handle")
+
+    def __init__(self, stream, like, name):
+        if not isinstance(like, torch.Tensor) or not like.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        self.device = like.get_device()
+        if self.device != torch.cuda.current_device():
+            raise ValueError(f"{name} is on cuda:{self.device}, but the current device is "
                              f"cuda:{torch.cuda.current_device()}")
         self.stream = stream
-        self.handle = _stream(stream)
+        self.handle = _raw_stream(self.device) if stream is None else stream.cuda_stream
 
-    def check(self, **tensors):
-        for name, t in tensors.items():
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+    def given(self, t, name, dtype, shape=None):
+        """The address of a caller's tensor, checked."""
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{self.device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
 
-    def empty(self, shape, dtype):
+    def empty(self, shape, dtype, like):
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape, dtype=dtype)
 
-    def workspace(self, nbytes, given):
+    def workspace(self, nbytes, given, like):
         if given is None:
-            return self.empty((nbytes,), torch.uint8)
-        _cuda(given, "workspace", torch.uint8)
-        self.check(workspace=given)
+            return self.empty(nbytes, torch.uint8, like)
+        self.given(given, "workspace", torch.uint8)
         if given.numel() < nbytes:
             raise ValueError(f"workspace needs {nbytes} bytes, got {given.numel()}")
         return given
-
-
-def _given(t, name, shape, dtype):
-    """A caller's output buffer, checked."""
-    _cuda(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
 
 
 # -------------------------------------------------------------------- route
@@ -851,26 +864,28 @@ def moe_grouped_swiglu_wgrad(x: torch.Tensor, hidden: torch.Tensor, dy: torch.Te
 
 # ------------------------------------------------------------------ RMS norm
 
-def _norm_args(x, weight, residual, residual_out, stream):
-    dt = _act(x, "x")
-    _cuda(weight, "weight", ndim=1)
-    if weight.dtype not in _DT:
-        raise ValueError(f"weight must be float32 or bfloat16, got {weight.dtype}")
-    if weight.shape[0] != x.shape[1]:
-        raise ValueError("weight must have H elements")
-    t = _Target(stream, x)
-    t.check(weight=weight)
-    if residual is not None:
-        _given(residual, "residual", x.shape, x.dtype)
-        t.check(residual=residual)
-        if residual_out is None:
-            residual_out = t.empty(x.shape, x.dtype)
-        else:
-            _given(residual_out, "residual_out", x.shape, x.dtype)
-            t.check(residual_out=residual_out)
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    return t, dt, _DT[weight.dtype], residual_out
+def _norm_rows(t, x, name, weight):
+    """(dtype codes of x [T,H] and weight [H], their addresses)."""
+    dtype, wdtype = x.dtype, weight.dtype if isinstance(weight, torch.Tensor) else None
+    if x.dim() != 2 or dtype not in _DT:
+        raise ValueError(f"{name} must be float32 or bfloat16 [T, H], got {dtype} with {x.dim()} dims")
+    if wdtype not in _DT:
+        raise ValueError(f"weight must be float32 or bfloat16, got {wdtype}")
+    return (_DT[dtype], _DT[wdtype], t.given(x, name, dtype),
+            t.given(weight, "weight", wdtype, x.shape[1:]))
+
+
+def _norm_residual(t, x, residual, residual_out):
+    """(h, address of residual or None, address of residual_out or None)."""
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return x, None, None
+    pr = t.given(residual, "residual", x.dtype, x.shape)
+    if residual_out is None:
+        residual_out = t.empty(x.shape, x.dtype, x)
+        return residual_out, pr, residual_out.data_ptr()
+    return residual_out, pr, t.given(residual_out, "residual_out", x.dtype, x.shape)
 
 
 def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -879,16 +894,19 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     """(y, h): h = x + residual as stored (x itself without a residual) and
     y = h / sqrt(mean(h^2) + eps) * weight.  out and residual_out may each be
     x or residual (the stream updated in place), but not the same tensor."""
-    t, dt, wdt, residual_out = _norm_args(x, weight, residual, residual_out, stream)
+    t = _Target(stream, x, "x")
+    dt, wdt, px, pw = _norm_rows(t, x, "x", weight)
+    h, pr, ph = _norm_residual(t, x, residual, residual_out)
     T, H = x.shape
     if out is None:
-        out = t.empty((T, H), x.dtype)
+        out = t.empty(x.shape, x.dtype, x)
+        po = out.data_ptr()
     else:
-        _given(out, "out", (T, H), x.dtype)
-        t.check(out=out)
-    _ok("moe_rmsnorm", load_library().moe_rmsnorm(
-        _p(x), _p(residual), dt, _p(weight), wdt, T, H, eps, _p(residual_out), _p(out), t.handle))
-    return out, x if residual is None else residual_out
+        po = t.given(out, "out", x.dtype, x.shape)
+    st = load_library().moe_rmsnorm(px, pr, dt, pw, wdt, T, H, eps, ph, po, t.handle)
+    if st:
+        raise MoeError("moe_rmsnorm", st)
+    return out, h
 
 
 def moe_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor,
@@ -898,21 +916,25 @@ def moe_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor,
     """(x_q float8_e4m3fn [T,H], scales float32 [T,H/block], h): moe_rmsnorm
     with y quantized from float32 as moe_quantize_fp8 does; out: an optional
     (x_q, scales) pair to write into."""
-    t, dt, wdt, residual_out = _norm_args(x, weight, residual, residual_out, stream)
+    t = _Target(stream, x, "x")
+    dt, wdt, px, pw = _norm_rows(t, x, "x", weight)
     T, H = x.shape
     if block <= 0 or H % block != 0:
         raise ValueError("H must be a multiple of block")
+    h, pr, ph = _norm_residual(t, x, residual, residual_out)
     if out is None:
-        q, sc = t.empty((T, H), torch.float8_e4m3fn), t.empty((T, H // block), torch.float32)
+        q = t.empty(x.shape, torch.float8_e4m3fn, x)
+        sc = t.empty((T, H // block), torch.float32, x)
+        pq, ps = q.data_ptr(), sc.data_ptr()
     else:
         q, sc = out
-        _given(q, "x_q", (T, H), torch.float8_e4m3fn)
-        _given(sc, "scales", (T, H // block), torch.float32)
-        t.check(x_q=q, scales=sc)
-    _ok("moe_rmsnorm_quantize_fp8", load_library().moe_rmsnorm_quantize_fp8(
-        _p(x), _p(residual), dt, _p(weight), wdt, T, H, eps, block, _p(residual_out), _p(q),
-        _p(sc), t.handle))
-    return q, sc, x if residual is None else residual_out
+        pq = t.given(q, "x_q", torch.float8_e4m3fn, x.shape)
+        ps = t.given(sc, "scales", torch.float32, (T, H // block))
+    st = load_library().moe_rmsnorm_quantize_fp8(px, pr, dt, pw, wdt, T, H, eps, block, ph, pq, ps,
+                                                 t.handle)
+    if st:
+        raise MoeError("moe_rmsnorm_quantize_fp8", st)
+    return q, sc, h
 
 
 def moe_rmsnorm_backward_workspace_size(T: int, H: int) -> int:
@@ -930,24 +952,26 @@ def moe_rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Te
     """(grad_x, grad_weight float32 [H]) of moe_rmsnorm from the h it returned;
     grad_h is the gradient of h from the residual stream.  grad_x, which is
     the gradient of x and of residual, may be grad_y, grad_h or h."""
-    t, dt, wdt, _ = _norm_args(h, weight, None, None, stream)
+    t = _Target(stream, h, "h")
+    dt, wdt, ph, pw = _norm_rows(t, h, "h", weight)
     T, H = h.shape
-    for g, name in ((grad_y, "grad_y"), (grad_h, "grad_h"), (grad_x, "grad_x")):
-        if g is not None:
-            _given(g, name, (T, H), h.dtype)
-    if grad_y is None:
-        raise ValueError("grad_y is needed")
-    t.check(grad_y=grad_y, grad_h=grad_h, grad_x=grad_x, grad_weight=grad_weight)
+    pg = t.given(grad_y, "grad_y", h.dtype, h.shape)
+    pgh = None if grad_h is None else t.given(grad_h, "grad_h", h.dtype, h.shape)
     if grad_x is None:
-        grad_x = t.empty((T, H), h.dtype)
-    if grad_weight is None:
-        grad_weight = t.empty((H,), torch.float32)
+        grad_x = t.empty(h.shape, h.dtype, h)
+        pgx = grad_x.data_ptr()
     else:
-        _given(grad_weight, "grad_weight", (H,), torch.float32)
-    ws = t.workspace(moe_rmsnorm_backward_workspace_size(T, H), workspace)
-    _ok("moe_rmsnorm_backward", load_library().moe_rmsnorm_backward(
-        _p(grad_y), _p(grad_h), _p(h), dt, _p(weight), wdt, T, H, eps, _p(grad_x),
-        _p(grad_weight), _p(ws), ws.numel(), t.handle))
+        pgx = t.given(grad_x, "grad_x", h.dtype, h.shape)
+    if grad_weight is None:
+        grad_weight = t.empty(H, torch.float32, h)
+        pgw = grad_weight.data_ptr()
+    else:
+        pgw = t.given(grad_weight, "grad_weight", torch.float32, h.shape[1:])
+    ws = t.workspace(moe_rmsnorm_backward_workspace_size(T, H), workspace, h)
+    st = load_library().moe_rmsnorm_backward(pg, pgh, ph, dt, pw, wdt, T, H, eps, pgx, pgw,
+                                             ws.data_ptr(), ws.numel(), t.handle)
+    if st:
+        raise MoeError("moe_rmsnorm_backward", st)
     return grad_x, grad_weight
 
 
@@ -960,29 +984,29 @@ def moe_layer_decode_workspace_size(T: int, E: int, k: int, H: int, I: int) -> i
     return n.value
 
 
-def _layer_args(x, x_scales, w_up_packed, w_down_packed, out, stream):
-    if x_scales is None:
-        _cuda(x, "x", torch.bfloat16, 2)
-    else:
-        _cuda(x, "x", torch.float8_e4m3fn, 2)
+def _layer_args(t, x, x_scales, w_up_packed, w_down_packed, out):
+    """(T, H, E, I, out, addresses of x, x_scales, the weights and out)."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, H], got {x.dim()} dims")
     T, H = x.shape
-    _cuda(w_up_packed, "w_up_packed", torch.bfloat16, 3)
-    _cuda(w_down_packed, "w_down_packed", torch.bfloat16, 3)
-    E, I2, H2 = w_up_packed.shape
-    I = I2 // 2
-    if H2 != H or I2 != 2 * I or tuple(w_down_packed.shape) != (E, H, I):
-        raise ValueError("packed weights do not match x")
-    if x_scales is not None:
+    if x_scales is None:
+        px, ps = t.given(x, "x", torch.bfloat16), None
+    else:
+        px = t.given(x, "x", torch.float8_e4m3fn)
         if H % 128:
             raise ValueError("H must be a multiple of the block of 128")
-        _given(x_scales, "x_scales", (T, H // 128), torch.float32)
-    t = _Target(stream, x)
-    t.check(x_scales=x_scales, w_up_packed=w_up_packed, w_down_packed=w_down_packed, out=out)
+        ps = t.given(x_scales, "x_scales", torch.float32, (T, H // 128))
+    pu = t.given(w_up_packed, "w_up_packed", torch.bfloat16)
+    if w_up_packed.dim() != 3 or w_up_packed.shape[2] != H or w_up_packed.shape[1] % 2:
+        raise ValueError("w_up_packed must be [E, 2I, H]")
+    E, I = w_up_packed.shape[0], w_up_packed.shape[1] // 2
+    pd = t.given(w_down_packed, "w_down_packed", torch.bfloat16, (E, H, I))
     if out is None:
-        out = t.empty((T, H), torch.bfloat16)
+        out = t.empty((T, H), torch.bfloat16, x)
+        po = out.data_ptr()
     else:
-        _given(out, "out", (T, H), torch.bfloat16)
-    return t, T, H, E, I, out
+        po = t.given(out, "out", torch.bfloat16, (T, H))
+    return T, H, E, I, out, px, ps, pu, pd, po
 
 
 def moe_layer_decode(x: torch.Tensor, logits: torch.Tensor, k: int, w_up_packed: torch.Tensor,
@@ -992,14 +1016,16 @@ def moe_layer_decode(x: torch.Tensor, logits: torch.Tensor, k: int, w_up_packed:
     """(out [T,H] bf16, topk_idx, topk_w): a whole MoE layer for up to 64
     tokens, from the router's logits [T,E].  x is bf16, or e4m3 with x_scales
     [T, H/128]; the weights are moe_grouped_swiglu_pack's."""
-    t, T, H, E, I, out = _layer_args(x, x_scales, w_up_packed, w_down_packed, out, stream)
-    _given(logits, "logits", (T, E), torch.float32)
-    t.check(logits=logits)
-    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace)
-    idx, w = t.empty((T, k), torch.int32), t.empty((T, k), torch.float32)
-    _ok("moe_layer_decode", load_library().moe_layer_decode(
-        _p(x), _p(x_scales), _p(logits), T, E, k, H, I, _p(w_up_packed), _p(w_down_packed),
-        _p(idx), _p(w), _p(out), _p(ws), ws.numel(), t.handle))
+    t = _Target(stream, x, "x")
+    T, H, E, I, out, px, ps, pu, pd, po = _layer_args(t, x, x_scales, w_up_packed, w_down_packed,
+                                                      out)
+    pl = t.given(logits, "logits", torch.float32, (T, E))
+    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace, x)
+    idx, w = t.empty((T, k), torch.int32, x), t.empty((T, k), torch.float32, x)
+    st = load_library().moe_layer_decode(px, ps, pl, T, E, k, H, I, pu, pd, idx.data_ptr(),
+                                         w.data_ptr(), po, ws.data_ptr(), ws.numel(), t.handle)
+    if st:
+        raise MoeError("moe_layer_decode", st)
     out._moe_workspace = ws
     return out, idx, w
 
@@ -1010,17 +1036,19 @@ def moe_layer_decode_indices(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: to
                              out: Optional[torch.Tensor] = None,
                              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [T,H] bf16 of moe_layer_decode for given choices (-1 = empty slot)."""
-    t, T, H, E, I, out = _layer_args(x, x_scales, w_up_packed, w_down_packed, out, stream)
-    _cuda(topk_idx, "topk_idx", torch.int32, 2)
-    if topk_idx.shape[0] != T:
-        raise ValueError("topk_idx must have one row per token")
+    t = _Target(stream, x, "x")
+    T, H, E, I, out, px, ps, pu, pd, po = _layer_args(t, x, x_scales, w_up_packed, w_down_packed,
+                                                      out)
+    pi = t.given(topk_idx, "topk_idx", torch.int32)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, k], one row per token")
     k = topk_idx.shape[1]
-    _given(topk_w, "topk_w", (T, k), torch.float32)
-    t.check(topk_idx=topk_idx, topk_w=topk_w)
-    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace)
-    _ok("moe_layer_decode_indices", load_library().moe_layer_decode_indices(
-        _p(x), _p(x_scales), _p(topk_idx), _p(topk_w), T, E, k, H, I, _p(w_up_packed),
-        _p(w_down_packed), _p(out), _p(ws), ws.numel(), t.handle))
+    pw = t.given(topk_w, "topk_w", torch.float32, (T, k))
+    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace, x)
+    st = load_library().moe_layer_decode_indices(px, ps, pi, pw, T, E, k, H, I, pu, pd, po,
+                                                 ws.data_ptr(), ws.numel(), t.handle)
+    if st:
+        raise MoeError("moe_layer_decode_indices", st)
     out._moe_workspace = ws
     return out
 
