@@ -209,7 +209,7 @@ class _Target:
     and the stream, for which outputs and workspaces are allocated (a tensor of
     another stream's pool could still be in use there)."""
 
-    __slots__ = ("device", "stream", "handle")
+    __slots__ = ("device", "where", "stream", "handle")
 
     def __init__(self, stream, like, name):
         if not isinstance(like, torch.Tensor) or not like.is_cuda:
@@ -218,6 +218,7 @@ class _Target:
         if self.device != torch.cuda.current_device():
             raise ValueError(f"{name} is on cuda:{self.device}, but the current device is "
                              f"cuda:{torch.cuda.current_device()}")
+        self.where = like.device
         self.stream = stream
         self.handle = _raw_stream(self.device) if stream is None else stream.cuda_stream
 
@@ -235,15 +236,21 @@ class _Target:
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def empty(self, shape, dtype, like):
+    def empty(self, shape, dtype):
         if self.stream is None:
-            return like.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self.where)
         with torch.cuda.stream(self.stream):
-            return like.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self.where)
 
-    def workspace(self, nbytes, given, like):
+    def empty_like(self, t):
+        if self.stream is None:
+            return torch.empty_like(t)
+        with torch.cuda.stream(self.stream):
+            return torch.empty_like(t)
+
+    def workspace(self, nbytes, given):
         if given is None:
-            return self.empty(nbytes, torch.uint8, like)
+            return self.empty(nbytes, torch.uint8)
         self.given(given, "workspace", torch.uint8)
         if given.numel() < nbytes:
             raise ValueError(f"workspace needs {nbytes} bytes, got {given.numel()}")
@@ -883,7 +890,7 @@ def _norm_residual(t, x, residual, residual_out):
         return x, None, None
     pr = t.given(residual, "residual", x.dtype, x.shape)
     if residual_out is None:
-        residual_out = t.empty(x.shape, x.dtype, x)
+        residual_out = t.empty_like(x)
         return residual_out, pr, residual_out.data_ptr()
     return residual_out, pr, t.given(residual_out, "residual_out", x.dtype, x.shape)
 
@@ -899,7 +906,7 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     h, pr, ph = _norm_residual(t, x, residual, residual_out)
     T, H = x.shape
     if out is None:
-        out = t.empty(x.shape, x.dtype, x)
+        out = t.empty_like(x)
         po = out.data_ptr()
     else:
         po = t.given(out, "out", x.dtype, x.shape)
@@ -923,8 +930,8 @@ def moe_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor,
         raise ValueError("H must be a multiple of block")
     h, pr, ph = _norm_residual(t, x, residual, residual_out)
     if out is None:
-        q = t.empty(x.shape, torch.float8_e4m3fn, x)
-        sc = t.empty((T, H // block), torch.float32, x)
+        q = t.empty(x.shape, torch.float8_e4m3fn)
+        sc = t.empty((T, H // block), torch.float32)
         pq, ps = q.data_ptr(), sc.data_ptr()
     else:
         q, sc = out
@@ -958,16 +965,16 @@ def moe_rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Te
     pg = t.given(grad_y, "grad_y", h.dtype, h.shape)
     pgh = None if grad_h is None else t.given(grad_h, "grad_h", h.dtype, h.shape)
     if grad_x is None:
-        grad_x = t.empty(h.shape, h.dtype, h)
+        grad_x = t.empty_like(h)
         pgx = grad_x.data_ptr()
     else:
         pgx = t.given(grad_x, "grad_x", h.dtype, h.shape)
     if grad_weight is None:
-        grad_weight = t.empty(H, torch.float32, h)
+        grad_weight = t.empty(H, torch.float32)
         pgw = grad_weight.data_ptr()
     else:
         pgw = t.given(grad_weight, "grad_weight", torch.float32, h.shape[1:])
-    ws = t.workspace(moe_rmsnorm_backward_workspace_size(T, H), workspace, h)
+    ws = t.workspace(moe_rmsnorm_backward_workspace_size(T, H), workspace)
     st = load_library().moe_rmsnorm_backward(pg, pgh, ph, dt, pw, wdt, T, H, eps, pgx, pgw,
                                              ws.data_ptr(), ws.numel(), t.handle)
     if st:
@@ -1002,7 +1009,7 @@ def _layer_args(t, x, x_scales, w_up_packed, w_down_packed, out):
     E, I = w_up_packed.shape[0], w_up_packed.shape[1] // 2
     pd = t.given(w_down_packed, "w_down_packed", torch.bfloat16, (E, H, I))
     if out is None:
-        out = t.empty((T, H), torch.bfloat16, x)
+        out = t.empty((T, H), torch.bfloat16)
         po = out.data_ptr()
     else:
         po = t.given(out, "out", torch.bfloat16, (T, H))
@@ -1020,8 +1027,8 @@ def moe_layer_decode(x: torch.Tensor, logits: torch.Tensor, k: int, w_up_packed:
     T, H, E, I, out, px, ps, pu, pd, po = _layer_args(t, x, x_scales, w_up_packed, w_down_packed,
                                                       out)
     pl = t.given(logits, "logits", torch.float32, (T, E))
-    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace, x)
-    idx, w = t.empty((T, k), torch.int32, x), t.empty((T, k), torch.float32, x)
+    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace)
+    idx, w = t.empty((T, k), torch.int32), t.empty((T, k), torch.float32)
     st = load_library().moe_layer_decode(px, ps, pl, T, E, k, H, I, pu, pd, idx.data_ptr(),
                                          w.data_ptr(), po, ws.data_ptr(), ws.numel(), t.handle)
     if st:
@@ -1044,7 +1051,7 @@ def moe_layer_decode_indices(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: to
         raise ValueError("topk_idx must be [T, k], one row per token")
     k = topk_idx.shape[1]
     pw = t.given(topk_w, "topk_w", torch.float32, (T, k))
-    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace, x)
+    ws = t.workspace(moe_layer_decode_workspace_size(T, E, k, H, I), workspace)
     st = load_library().moe_layer_decode_indices(px, ps, pi, pw, T, E, k, H, I, pu, pd, po,
                                                  ws.data_ptr(), ws.numel(), t.handle)
     if st:
