@@ -254,6 +254,38 @@ __device__ __forceinline__ void route(const LayerArgs& a, const Routing& r, bool
         }
         __syncthreads();
     }
+    if (n <= 32 && T <= 8) {
+        // Few choices: a warp has one in each lane, and the experts in the order of
+        // their first choices.  A unit takes all of an expert's tokens.
+        if (warp == 0) {
+            const int e = lane < n ? r.expert[lane] : -1;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, e < 0 ? -1 - lane : e);
+            const unsigned below = (1u << lane) - 1u;
+            const bool leads = e >= 0 && !(same & below);
+            const int c = leads ? __popc(same) : 0, unit = __popc(__ballot_sync(0xFFFFFFFFu, leads) & below);
+            int slot = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, slot, o);
+                if (lane >= o) slot += v;
+            }
+            slot = __shfl_sync(0xFFFFFFFFu, slot - c, __ffs(int(same)) - 1) + __popc(same & below);
+            if (leads) {
+                r.first[e] = uint16_t(slot);
+                r.units[e] = uint16_t(unit);
+                r.unit[unit] = uint16_t(e);
+                r.group[unit] = 0;
+            }
+            if (e >= 0) {
+                r.token[slot] = uint8_t(lane / k);
+                r.choice[slot] = uint16_t(lane);
+            }
+            const int units = __popc(__ballot_sync(0xFFFFFFFFu, leads));
+            if (lane == 0) { r.count[0] = units; r.count[2] = 8; }
+        }
+        __syncthreads();
+        return;
+    }
     // Prefix sums over the experts, `mine` of them a thread: tokens, and units of
     // 8, 16, 32 or 64 tokens.  Two sums to a word; each is at most 2048.
     const int mine = (E + kThreads - 1) / kThreads, e0 = min(threadIdx.x * mine, E);
@@ -388,6 +420,7 @@ struct Work {
 // Rounds that `items` take.
 __device__ __forceinline__ int rounds(int items) { return (items + int(gridDim.x) - 1) / int(gridDim.x); }
 
+// (A whole warp.)
 __device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r, int ring_bytes, bool up) {
     Work w;
     w.units = r.count[0];
@@ -397,15 +430,13 @@ __device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r, in
     const int tiles = w.units * w.strips, rest = tiles % int(gridDim.x);
     w.whole = tiles - rest;
     // An item's own cost is taken as 16 of the 64 columns, and as half a step of
-    // 128 of K.  No more than two rounds of parts: that bounds the workspace.
-    const int steps = a.I / 128;
-    int best = 0x7FFFFFFF;
-    w.cuts = 1;
-#pragma unroll 1
-    for (int c = 1; up ? c <= 4 : c <= min(kMaxParts, steps) && c * rest <= 2 * int(gridDim.x); c = up ? 2 * c : c + 1) {
-        const int cost = rounds(rest * c) * (up ? 64 / c + 16 : 2 * ((steps + c - 1) / c) + 1);
-        if (cost < best) { best = cost; w.cuts = c; }
-    }
+    // 128 of K.  No more than two rounds of parts: that bounds the workspace.  A
+    // lane tries each number of cuts.
+    const int c = up ? 1 << (lane_id() & 3) : 1 + int(lane_id() & 7), steps = a.I / 128;
+    const bool may = up ? c <= 4 : c == 1 || (c <= min(kMaxParts, steps) && c * rest <= 2 * int(gridDim.x));
+    const int cost = rounds(rest * c) * (up ? 64 / c + 16 : 2 * ((steps + c - 1) / c) + 1);
+    // the cheapest, of equal ones the fewest cuts
+    w.cuts = int(__reduce_min_sync(0xFFFFFFFFu, may ? uint32_t(cost) << 4 | uint32_t(c) : 0xFFFFFFFFu) & 15u);
     w.items = w.whole + rest * w.cuts;
     const int rows = up && w.whole == 0 ? kM / w.cuts : kM;    // of the largest item
     // As much of a row in one stage, 512 bytes, as leaves three stages: rows are
@@ -617,8 +648,10 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     }
     tc_fence_before();
     route(a, r, a.logits && blockIdx.x == 0);
-    if (warp >= kWarps - 2 && lane == 0)                   // two warps that may have no choices
-        s_work[warp & 1] = work_of(a, r, ring_bytes, (warp & 1) == 0);
+    if (warp >= kWarps - 2) {                              // two warps that may have no choices
+        const Work w = work_of(a, r, ring_bytes, (warp & 1) == 0);
+        if (lane == 0) s_work[warp & 1] = w;
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
@@ -638,14 +671,29 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
             for (int phase = 0; phase < 2; ++phase) {
                 const bool up = phase == 0;
                 const Work w = s_work[phase];
+                // A stage's weights, from sub-tile k on: gate rows and the matching up rows
+                // (blocks of 128 each), or rows of Wd.
+                auto copy = [&](const Work& w, const Item& m, int k, uint32_t dst, uint32_t bar) {
+                    const int row = up ? m.e * 2 * a.I + m.col / 128 * 256 + m.col % 128
+                                       : m.e * a.H + m.strip * kM;
+                    const int row2 = row + (up ? 128 : kM / 2), half = m.cols;
+                    const int box = half == kBigBox ? kBigBox : kSmallBox;
+                    const CUtensorMap* map = !up ? &map_down : half == kBigBox ? &map_up : &map_up_small;
+#pragma unroll 1
+                    for (int u = 0; u < min(w.subs, m.k1 - k); ++u) {
+                        const int c = (k + u) * 64;
+                        const uint32_t to = dst + u * w.a_sub;
+#pragma unroll 1
+                        for (int b = 0; b < half; b += box) {
+                            tma_load_2d_hint(to + b * 128, map, c, row + b, bar, once);
+                            tma_load_2d_hint(to + (half + b) * 128, map, c, row2 + b, bar, once);
+                        }
+                    }
+                };
                 uint32_t it = 0;
 #pragma unroll 1
                 for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x) {
                     const Item m = item_of(w, r, i, up);
-                    // gate rows and the matching up rows (blocks of 128 each), or rows of Wd
-                    const int row = up ? m.e * 2 * a.I + m.col / 128 * 256 + m.col % 128
-                                       : m.e * a.H + m.strip * kM;
-                    const int row2 = row + (up ? 128 : kM / 2), half = m.cols;
 #pragma unroll 1
                     for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
                         const int s = it % w.stages;
@@ -654,21 +702,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                             break;
                         }
                         const uint32_t bar = smem_addr(&full_a[phase][s]);
-                        const int subs = min(w.subs, m.k1 - k);
-                        mbar_expect_tx(bar, subs * half * 256);
-#pragma unroll 1
-                        for (int u = 0; u < subs; ++u) {
-                            const uint32_t dst = smem_addr(ring + s * w.stage_bytes + u * w.a_sub);
-                            const int c = (k + u) * 64;
-                            const int box = half == kBigBox ? kBigBox : kSmallBox;
-                            const CUtensorMap* map = !up ? &map_down
-                                                     : half == kBigBox ? &map_up : &map_up_small;
-#pragma unroll 1
-                            for (int b = 0; b < half; b += box) {
-                                tma_load_2d_hint(dst + b * 128, map, c, row + b, bar, once);
-                                tma_load_2d_hint(dst + (half + b) * 128, map, c, row2 + b, bar, once);
-                            }
-                        }
+                        mbar_expect_tx(bar, min(w.subs, m.k1 - k) * m.cols * 256);
+                        copy(w, m, k, smem_addr(ring + s * w.stage_bytes), bar);
                     }
                 }
                 // The ring takes another shape once its MMAs have read it.  A block
