@@ -9,6 +9,7 @@ from unpermute_combine_gb300 import build as libbuild
 P = ctypes.c_void_p
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 fake = P(0x1000)                 # never dereferenced: validation fails first
+other = P(0x8000)
 
 
 @pytest.fixture(scope="module")
@@ -18,12 +19,12 @@ def lib():
 
 
 def logits(lib, x=fake, xs=None, lg=fake, T=4, E=8, k=2, H=256, I=128, up=fake, down=fake, idx=fake,
-           w=fake, out=fake, ws=fake, n=1 << 30):
+           w=fake, out=other, ws=fake, n=1 << 30):
     return lib.moe_layer_decode(x, xs, lg, T, E, k, H, I, up, down, idx, w, out, ws, n, None)
 
 
 def choices(lib, x=fake, xs=None, idx=fake, w=fake, T=4, E=8, k=2, H=256, I=128, up=fake, down=fake,
-            out=fake, ws=fake, n=1 << 30):
+            out=other, ws=fake, n=1 << 30):
     return lib.moe_layer_decode_indices(x, xs, idx, w, T, E, k, H, I, up, down, out, ws, n, None)
 
 
@@ -31,7 +32,8 @@ def choices(lib, x=fake, xs=None, idx=fake, w=fake, T=4, E=8, k=2, H=256, I=128,
 def test_refusals(lib, call):
     for kw in (dict(T=-1), dict(E=0), dict(k=0), dict(H=0), dict(I=0), dict(x=None), dict(up=None),
                dict(down=None), dict(out=None), dict(idx=None), dict(w=None), dict(x=P(0x1008)),
-               dict(up=P(0x1008)), dict(down=P(0x1004)), dict(out=P(0x1002))):
+               dict(up=P(0x1008)), dict(down=P(0x1004)), dict(out=P(0x1002)),
+               dict(x=P(0x2000), out=P(0x2000))):
         assert call(lib, **kw) == INVALID, kw
     for kw in (dict(T=65), dict(E=1025, k=2), dict(k=9), dict(E=64, k=33), dict(H=128), dict(H=300),
                dict(I=64), dict(I=130), dict(E=1024, I=1 << 20)):

@@ -262,6 +262,71 @@ def test_graphs_that_share_a_workspace_and_another_stream():
     assert all(torch.equal(out, ref) for (_, out), (_, ref) in zip(graphs, sets))
 
 
+def test_two_calls_at_once():
+    """On two streams with a workspace each, one behind the other on the GPU."""
+    layer = Layer(32, 512, 256, 21)
+    rng = np.random.default_rng(22)
+    sets = []
+    for T, fp8 in ((9, False), (40, True)):
+        args, _ = _x(rng, T, 512, fp8)
+        logits = to_dev(rng.standard_normal((T, 32)).astype(np.float32))
+        sets.append(dict(logits=logits, k=4, w_up_packed=layer.up_p, w_down_packed=layer.down_p, **args))
+    refs = [moe.moe_layer_decode(**kw)[0] for kw in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [[], []]
+    for _ in range(10):
+        for kw, s, o in zip(sets, streams, outs):
+            o.append(moe.moe_layer_decode(**kw, stream=s)[0])
+    torch.cuda.synchronize()
+    for o, ref in zip(outs, refs):
+        assert all(torch.equal(v, ref) for v in o)
+        assert all(moe.moe_workspace_status(v._moe_workspace) == 0 for v in o)
+
+
+def test_a_workspace_that_another_call_wrote():
+    """The norm's backward and the router leave their data in a workspace; the
+    layer takes it as it is, and the other way round."""
+    layer = Layer(16, 512, 256, 23)
+    rng = np.random.default_rng(24)
+    args, _ = _x(rng, 20, 512, False)
+    logits = to_dev(rng.standard_normal((20, 16)).astype(np.float32))
+    kw = dict(logits=logits, k=3, w_up_packed=layer.up_p, w_down_packed=layer.down_p, **args)
+    ref = moe.moe_layer_decode(**kw)[0]
+    n = max(moe.moe_layer_decode_workspace_size(20, 16, 3, 512, 256),
+            moe.moe_rmsnorm_backward_workspace_size(700, 512), moe.moe_route_workspace_size(20, 16, 3))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    g = torch.randn((700, 512), device="cuda")
+    w = torch.ones(512, device="cuda")
+    gw = moe.moe_rmsnorm_backward(g, g, w)[1]
+    idx = moe.moe_route(logits, 3).topk_idx
+    for _ in range(3):
+        assert torch.equal(moe.moe_layer_decode(**kw, workspace=ws)[0], ref)
+        assert torch.equal(moe.moe_rmsnorm_backward(g, g, w, workspace=ws)[1], gw)
+        assert torch.equal(moe.moe_layer_decode(**kw, workspace=ws)[0], ref)
+        assert torch.equal(moe.moe_route(logits, 3, workspace=ws).topk_idx, idx)
+
+
+def test_logits_that_are_no_numbers():
+    """NaN and infinite logits (which the header excludes) touch no other token,
+    and every chosen id is one of the experts, or -1."""
+    layer = Layer(12, 256, 128, 25)
+    args, _ = _x(np.random.default_rng(26), 20, 256, False)
+    for T in (3, 20):
+        logits = np.random.default_rng(27).standard_normal((T, 12)).astype(np.float32)
+        kw = dict(k=4, w_up_packed=layer.up_p, w_down_packed=layer.down_p, x=args["x"][:T])
+        clean, cidx, _ = moe.moe_layer_decode(logits=to_dev(logits), **kw)
+        logits.view(np.uint32)[1] = 0xFFFFFFFF                 # the lowest of all bit patterns
+        logits[2] = -np.inf
+        out, idx, _ = moe.moe_layer_decode(logits=to_dev(logits), **kw)
+        keep = [t for t in range(T) if t not in (1, 2)]
+        assert torch.equal(idx[keep], cidx[keep])
+        assert ((idx >= -1) & (idx < 12)).all()
+        # another grouping of the experts' tokens sums in another order: 2^-8 and a bit
+        a, b = out[keep].float(), clean[keep].float()
+        assert torch.isfinite(a).all() and (a - b).abs().max() <= 2.0 ** -7 * b.abs().max()
+
+
 def test_agrees_with_the_dispatch_path():
     """route, permute, moe_grouped_swiglu and combine of the same tokens.  There
     the hidden rows and the experts' outputs are rounded to bf16: half a step of

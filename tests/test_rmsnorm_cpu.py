@@ -43,6 +43,7 @@ def test_shared_refusals(lib, call):
 def test_norm(lib):
     assert norm(lib, x=None) == INVALID and norm(lib, out=None) == INVALID
     assert norm(lib, res=fake) == INVALID                      # nowhere to store the sum
+    assert norm(lib, res=fake, ho=fake, out=fake) == INVALID   # two outputs in one place
     assert norm(lib, x=None, w=None, out=None, T=0) == OK
     assert norm(lib, x=None, w=None, out=None, H=0) == OK
 

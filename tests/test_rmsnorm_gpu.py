@@ -140,6 +140,21 @@ def test_norm_leaves_what_lies_behind():
     assert (out[T:] == 7).all() and (ho[T:] == 7).all()
 
 
+def test_more_rows_than_blocks():
+    """Over a million rows: the blocks go round.  Rows are computed alike wherever
+    they are, so parts of the tensor by themselves give the same bits."""
+    T, H = (1 << 20) + 7, 1048
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.rand((H,), generator=g, device="cuda").bfloat16()
+    y, _ = moe.moe_rmsnorm(x, w)
+    for a in (0, (1 << 20) - 500, T - 400):
+        assert torch.equal(y[a:a + 400], moe.moe_rmsnorm(x[a:a + 400], w)[0])
+    h64 = x[-3:].double()
+    ref = h64 / ((h64 * h64).mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
+    assert ((y[-3:].double() - ref).abs() <= ((_depth(H) / 2 + 8) * U + HALF["bf16"]) * ref.abs()).all()
+
+
 def test_special_rows():
     """A zero row gives zeros; a NaN makes its own row NaN and no other; eps = 0."""
     T, H = 4, 512

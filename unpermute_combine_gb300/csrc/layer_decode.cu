@@ -31,8 +31,8 @@
 // Every block works the routing out for itself (top-k, softmax, each expert's
 // tokens) in shared memory: a launch of its own would take longer.
 // Measured (one call after another in a CUDA graph, other weights each time): one
-// token, 6 of 64 experts, H = 2048, I = 1408: 35 us, of which 11 + 5 stream the
-// weights; the rest is latency (routing 5 us, the two meetings, the last sum).
+// token, 6 of 64 experts, H = 2048, I = 1408: 34.6 us, of which 11 + 5 stream the
+// weights; the rest is latency (routing 4 us, the two meetings, the last sum).
 // 16 tokens of these: 132 us, 6.2 TB/s; 64 tokens over 256 experts, H = 7168,
 // I = 2048: 2.83 ms, 6.9 TB/s (a copy on the same GPU: 6.7).  Three launches, with
 // the down projections' overlapping the up projections' (35, 139 us and 2.82 ms),
@@ -84,7 +84,7 @@ struct LayerArgs {
     uint64_t nonce;             // another one for each call from the host
     uint16_t* hidden;           // [2][T*k, I] bf16: the values, and what they leave
     float* y;                   // [T*k, H], a row for each choice
-    float* parts;               // [2 * kMaxBlocks][min(group, T)][kM]: the tiles that are cut
+    float* parts;               // [2 * kMaxBlocks][min(group, T)][kM]: tiles that are cut
     int T, E, k;
     int H, I;
 };
@@ -200,7 +200,7 @@ __device__ __forceinline__ void choose(const LayerArgs& a, const Routing& r, int
                 for (int i = 0; i < NV; ++i)
                     if (i == at) key[i] = 0u;
             }
-            if (lane == j) { my_key = top; my_id = e < a.E ? e : -1; }
+            if (lane == j) { my_key = top; my_id = top != 0u ? e : -1; }   // (0: no key is left)
         }
         // lane j has choice j; their softmax
         const float v = key_logit(my_key), v0 = __shfl_sync(0xFFFFFFFFu, v, base);
@@ -977,7 +977,8 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     if (st != MOE_OK) return st;
     const Layout l = workspace_layout(T, a.k, H, I);
     const bool choices = a.logits ? a.topk_idx && a.topk_w : a.given_idx && a.given_w;
-    if (T > 0 && (!a.x || !choices || !w_up || !w_down || !a.out)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!a.x || !choices || !w_up || !w_down || !a.out || a.out == a.x))
+        return MOE_ERR_INVALID_ARG;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) ||
         workspace_bytes < l.total)
         return MOE_ERR_WORKSPACE;
@@ -1015,8 +1016,11 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_kernel, up, up_small, down, a) == cudaSuccess
-               ? MOE_OK : MOE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, layer_kernel, up, up_small, down, a) != cudaSuccess) {
+        cudaGetLastError();                                // not the next call's
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
 }  // namespace

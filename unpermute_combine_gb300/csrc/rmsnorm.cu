@@ -870,7 +870,8 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, moe_dty
     const moe_status_t st = check_norm(dtype, weight_dtype, T, H, eps);
     if (st != MOE_OK) return st;
     if (T == 0 || H == 0) return MOE_OK;
-    if (!x || !weight || !out || (residual && !residual_out)) return MOE_ERR_INVALID_ARG;
+    if (!x || !weight || !out || (residual && (!residual_out || residual_out == out)))
+        return MOE_ERR_INVALID_ARG;
     if (!residual) residual_out = nullptr;
     const NormArgs a{x, residual, weight, residual_out, out, nullptr, T, H, eps, 0};
     const Rows how = rows_of(H, weight, {x, residual, residual_out, out});
