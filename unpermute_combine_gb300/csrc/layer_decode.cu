@@ -413,6 +413,7 @@ struct Work {
     int group;                  // tokens of a B tile
     int subs, shift, ksubs;     // sub-tiles (64 of K) of a stage, its logarithm; of all K
     int stage_bytes, stages;
+    int teams, team;            // of loader warps, a stage each; warps of one
     int a_sub, b_sub;           // bytes of a sub-tile
     bool two;                   // the B rows come in two bf16 parts
 };
@@ -439,19 +440,19 @@ __device__ __forceinline__ Work work_of(const LayerArgs& a, const Routing& r, in
     w.cuts = int(__reduce_min_sync(0xFFFFFFFFu, may ? uint32_t(cost) << 4 | uint32_t(c) : 0xFFFFFFFFu) & 15u);
     w.items = w.whole + rest * w.cuts;
     const int rows = up && w.whole == 0 ? kM / w.cuts : kM;    // of the largest item
-    // As much of a row in one stage, 512 bytes, as leaves three stages: rows are
-    // far apart, and memory is slower the shorter the pieces (16 tokens, 64
-    // experts, H = 2048: 154 us with 128 bytes, 135 with 256, 132 with 512).  Large
-    // groups have long gathers instead, one warp a stage, and want many stages
-    // (64 tokens, 8 of 8 experts: 208 us with three stages, 149 with nine).
+    // As much of a row in one stage, up to 512 bytes, as leaves three stages: rows
+    // are far apart, and memory is slower the shorter the pieces (16 tokens, 64
+    // experts, H = 2048: 154 us with 128 bytes, 135 with 256, 132 with 512).
     w.a_sub = rows * 128;
     w.b_sub = w.two ? w.group * 256 : max(w.group, 16) * 128;
     const int sub = w.a_sub + w.b_sub;
     const int left = ring_bytes - (kM - rows) * 128;       // an MMA reads kM rows all the same
-    w.shift = w.group > 16 ? 0 : 12 * sub <= left ? 2 : 1;
+    w.shift = 12 * sub <= left ? 2 : 6 * sub <= left ? 1 : 0;
     w.subs = 1 << w.shift;
     w.stage_bytes = w.subs * sub;
     w.stages = min(kMaxStages, left / w.stage_bytes);
+    w.teams = min(kLoaders, w.stages);
+    w.team = kLoaders / w.teams;
     w.ksubs = (up ? a.H : a.I) / 64;
     return w;
 }
@@ -622,7 +623,6 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     if (threadIdx.x < 2 * kMaxStages) {
         const int p = threadIdx.x / kMaxStages, s = threadIdx.x % kMaxStages;
         mbar_init(smem_addr(&full_a[p][s]), 1);
-        mbar_init(smem_addr(&full_b[p][s]), 1);
         mbar_init(smem_addr(&empty[p][s]), 1);
         if (s < 2) {
             mbar_init(smem_addr(p ? &acc_full[s] : &acc_empty[s]), p ? 1 : 128);
@@ -651,6 +651,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     if (warp >= kWarps - 2) {                              // two warps that may have no choices
         const Work w = work_of(a, r, ring_bytes, (warp & 1) == 0);
         if (lane == 0) s_work[warp & 1] = w;
+        if (lane < kMaxStages) mbar_init(smem_addr(&full_b[warp & 1][lane]), w.team);
+        mbar_fence_init();
     }
     __syncthreads();
     tc_fence_after();
@@ -777,10 +779,11 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         for (int phase = 0; phase < 2 && !stop; ++phase) {
             const bool up = phase == 0;
             const Work w = s_work[phase];
-            // No more warps than stages: a warp that waits for a stage has seen the
-            // use before its own last one end, so the stage's barrier can be at most
-            // one phase behind and the parity is not mistaken for an older one.
-            const uint32_t loaders = min(kLoaders, w.stages), mine = warp - 2;
+            // No more teams than stages: a warp that waits for a stage has seen the use
+            // before its own last one end, so the stage's barrier can be at most one
+            // phase behind and the parity is not mistaken for an older one.
+            const int mine = (warp - 2) / w.team, member = (warp - 2) - mine * w.team;
+            if (mine >= w.teams) continue;
             const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
             uint32_t it = 0;
             bool met = up;
@@ -790,7 +793,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                 const int chunks = m.n * row_chunks, part2 = b_rows(m.n, w.two) * 128;
 #pragma unroll 1
                 for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
-                    if (it % loaders != mine) continue;
+                    if (int(it % w.teams) != mine) continue;
                     const int s = it % w.stages;
                     uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
                     bool ready = false;
@@ -800,8 +803,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                         met = true;
                     }
 #pragma unroll 1
-                    for (int c0 = 0; c0 < chunks; c0 += 32 * kFly) {
-                        // the first chunks are loaded before the wait
+                    for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
+                        // the first chunks (a warp may have none) are loaded before the wait
                         uint4 v[kFly], v2[kFly];
                         float sc[kFly];
 #pragma unroll
