@@ -13,10 +13,12 @@
 //   warp 0        TMA producer: stages of weight rows x up to 256 of K, in a
 //                 ring that fills the SM's shared memory
 //   warp 1        one thread issues the MMAs
-//   warps 2..10   fill the B tiles: gathered token rows (e4m3 codes times their
-//                 scale) or hidden rows, one warp a stage, so that the latency
-//                 of several gathers overlaps (warp 2 also has the tensor memory)
-//   warp 11       waits for the other blocks
+//   warps 2..10   fill the up phase's B tiles with gathered token rows (e4m3 codes
+//                 times their scale), one or several warps a stage, so that the
+//                 latency of several gathers overlaps (warp 2 also has the tensor
+//                 memory)
+//   warp 11       waits for the other blocks, and copies hidden rows into the down
+//                 phase's B tiles
 //   warps 12..15  epilogue: silu(gate) * up, or the down products
 // Precision: the MMA's operands are bf16, but a hidden value, and an e4m3 code
 // times its scale, are not bf16 values.  Both are split into a bf16 value and
@@ -50,6 +52,7 @@ namespace {
 constexpr int kMaxTokens = 64;
 constexpr int kM = 128;                   // rows of an MMA, weight rows of a down tile
 constexpr int kBigBox = 64, kSmallBox = 16;    // weight rows of a TMA box
+constexpr int kRowBox = 8, kRowBigBox = 32;    // hidden rows of one
 constexpr int kMaxStages = 16;
 constexpr int kLoaders = 9;               // warps that fill B tiles
 constexpr int kThreads = 512, kWarps = kThreads / 32;
@@ -598,11 +601,12 @@ __device__ __forceinline__ void add_up(const LayerArgs& a, const Routing& r, con
 
 __global__ void __launch_bounds__(kThreads, 1)
 layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_up_small,
-             const __grid_constant__ CUtensorMap map_down, const LayerArgs a) {
+             const __grid_constant__ CUtensorMap map_down, const __grid_constant__ CUtensorMap map_hidden,
+             const __grid_constant__ CUtensorMap map_hidden_big, const LayerArgs a) {
     extern __shared__ uint8_t smem_raw[];
     // a phase has its own barriers of the ring, and a ring of its own shape
     __shared__ __align__(8) uint64_t full_a[2][kMaxStages], full_b[2][kMaxStages], empty[2][kMaxStages];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], hidden_there;
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
     __shared__ uint32_t s_tmem;
     __shared__ uint64_t s_token;
     __shared__ volatile int s_failed;
@@ -627,7 +631,6 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         if (s < 2) {
             mbar_init(smem_addr(p ? &acc_full[s] : &acc_empty[s]), p ? 1 : 128);
         } else if (threadIdx.x == 2) {
-            mbar_init(smem_addr(&hidden_there), 1);
             s_failed = 0;
         }
         mbar_fence_init();
@@ -636,6 +639,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
             prefetch_map(&map_up);
             prefetch_map(&map_up_small);
             prefetch_map(&map_down);
+            prefetch_map(&map_hidden);
+            prefetch_map(&map_hidden_big);
         }
     } else if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -651,7 +656,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     if (warp >= kWarps - 2) {                              // two warps that may have no choices
         const Work w = work_of(a, r, ring_bytes, (warp & 1) == 0);
         if (lane == 0) s_work[warp & 1] = w;
-        if (lane < kMaxStages) mbar_init(smem_addr(&full_b[warp & 1][lane]), w.team);
+        if (lane < kMaxStages) mbar_init(smem_addr(&full_b[warp & 1][lane]), (warp & 1) ? 1 : w.team);
         mbar_fence_init();
     }
     __syncthreads();
@@ -768,87 +773,110 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
             }
         }
     } else if (warp == kEpilogue - 1) {
-        // --------------------------------------------- waits for the other blocks
+        // ------------------------------ waits for the other blocks; B tiles, down phase
         if (!wait_for_blocks(a, 0, s_token)) s_failed = 1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&hidden_there));
-    } else if (warp < 2 + kLoaders) {
-        // ----------------------------------------------------------- B loaders
-        bool stop = false;                                 // the same in all lanes
-#pragma unroll 1
-        for (int phase = 0; phase < 2 && !stop; ++phase) {
-            const bool up = phase == 0;
-            const Work w = s_work[phase];
-            // No more teams than stages: a warp that waits for a stage has seen the use
-            // before its own last one end, so the stage's barrier can be at most one
-            // phase behind and the parity is not mistaken for an older one.
-            const int mine = (warp - 2) / w.team, member = (warp - 2) - mine * w.team;
-            if (mine >= w.teams) continue;
-            const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
+        if (lane == 0) {
+            // the hidden rows, which other blocks' threads wrote and copies now read
+            asm volatile("fence.proxy.async;" ::: "memory");
+            const Work w = s_work[1];
             uint32_t it = 0;
-            bool met = up;
 #pragma unroll 1
-            for (int i = blockIdx.x; i < w.items && !stop; i += gridDim.x) {
-                const Item m = item_of(w, r, i, up);
-                const int chunks = m.n * row_chunks, part2 = b_rows(m.n, w.two) * 128;
+            for (int i = blockIdx.x; i < w.items && !s_failed; i += gridDim.x) {
+                const Item m = item_of(w, r, i, false);
+                const int rows = b_rows(m.n, true);        // (a row more than n is another unit's)
 #pragma unroll 1
                 for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
-                    if (int(it % w.teams) != mine) continue;
-                    const int s = it % w.stages;
-                    uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
-                    bool ready = false;
-                    if (!met) {
-                        // every block's hidden rows
-                        if (!bar_wait(smem_addr(&hidden_there), 0)) s_failed = 1;
-                        met = true;
+                    const int s = it % w.stages, subs = min(w.subs, m.k1 - k);
+                    if (!bar_wait(smem_addr(&empty[1][s]), ((it / w.stages) & 1u) ^ 1u)) {
+                        s_failed = 1;
+                        break;
                     }
+                    const uint32_t bar = smem_addr(&full_b[1][s]);
+                    mbar_expect_tx(bar, subs * rows * 256);
 #pragma unroll 1
-                    for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
-                        // the first chunks (a warp may have none) are loaded before the wait
-                        uint4 v[kFly], v2[kFly];
-                        float sc[kFly];
-#pragma unroll
-                        for (int q = 0; q < kFly; ++q) {
-                            const int c = c0 + q * 32 + lane, row = m.first + (c >> row_shift);
-                            const int col = k * 64 + (c & (row_chunks - 1)) * 8;
-                            if (c >= chunks || col >= m.k1 * 64) continue;
-                            if (!up) {
-                                const uint16_t* p = a.hidden + int64_t(row) * a.I + col;
-                                v[q] = __ldcg(reinterpret_cast<const uint4*>(p));
-                                v2[q] = __ldcg(reinterpret_cast<const uint4*>(p + int64_t(a.T) * a.k * a.I));
-                            } else if (!a.x_scales) {
-                                v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) +
-                                                int64_t(r.token[row]) * a.H + col);
-                            } else {
-                                const int t = r.token[row];
-                                const uint2 code = __ldg(reinterpret_cast<const uint2*>(
-                                    static_cast<const uint8_t*>(a.x) + int64_t(t) * a.H + col));
-                                v[q].x = code.x;
-                                v[q].y = code.y;
-                                sc[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
-                            }
-                        }
-                        if (!ready) {
-                            ready = bar_wait(smem_addr(&empty[phase][s]), ((it / w.stages) & 1u) ^ 1u);
-                            if (!ready) { s_failed = 1; break; }
-                        }
-#pragma unroll
-                        for (int q = 0; q < kFly; ++q) {
-                            const int c = c0 + q * 32 + lane, row = c >> row_shift;
-                            const int j = c & (row_chunks - 1);
-                            if (c >= chunks || k * 8 + j >= m.k1 * 8) continue;
-                            if (up && w.two) split_codes(make_uint2(v[q].x, v[q].y), sc[q], v[q], v2[q]);
-                            uint8_t* sub = tile + (j >> 3) * w.b_sub;
-                            put_chunk(sub, row, j & 7, v[q]);
-                            if (w.two) put_chunk(sub + part2, row, j & 7, v2[q]);
+                    for (int u = 0; u < subs; ++u) {
+                        const uint32_t dst = smem_addr(ring + s * w.stage_bytes + w.subs * w.a_sub + u * w.b_sub);
+#pragma unroll 1
+                        for (int b = 0; b < rows;) {
+                            const bool big = rows - b >= kRowBigBox;
+                            const CUtensorMap* map = big ? &map_hidden_big : &map_hidden;
+                            tma_load_2d(dst + b * 128, map, (k + u) * 64, m.first + b, bar);
+                            tma_load_2d(dst + (rows + b) * 128, map, (k + u) * 64,
+                                        a.T * a.k + m.first + b, bar);
+                            b += big ? kRowBigBox : kRowBox;
                         }
                     }
-                    // each thread orders its writes before the tensor core's reads
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    stop = __any_sync(0xFFFFFFFFu, s_failed != 0);
-                    if (stop) break;
-                    if (lane == 0) mbar_arrive(smem_addr(&full_b[phase][s]));
                 }
+            }
+            if (s_failed)                                  // none of its copies stays in flight
+                for (uint32_t b = it > uint32_t(w.stages) ? it - w.stages : 0; b < it; ++b)
+                    bar_wait(smem_addr(&full_b[1][b % w.stages]), (b / w.stages) & 1u);
+        }
+    } else if (warp < 2 + kLoaders) {
+        // -------------------------------------------------- B loaders, up phase
+        const Work w = s_work[0];
+        // No more teams than stages: a warp that waits for a stage has seen the use
+        // before its own last one end, so the stage's barrier can be at most one phase
+        // behind and the parity is not mistaken for an older one.
+        const int mine = (warp - 2) / w.team, member = (warp - 2) - mine * w.team;
+        const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
+        uint32_t it = 0;
+        bool stop = mine >= w.teams;                       // the same in all lanes
+#pragma unroll 1
+        for (int i = blockIdx.x; i < w.items && !stop; i += gridDim.x) {
+            const Item m = item_of(w, r, i, true);
+            const int chunks = m.n * row_chunks, part2 = b_rows(m.n, w.two) * 128;
+#pragma unroll 1
+            for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
+                if (int(it % w.teams) != mine) continue;
+                const int s = it % w.stages;
+                uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
+                bool ready = false;
+#pragma unroll 1
+                for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
+                    // the first chunks (a warp may have none) are loaded before the wait
+                    uint4 v[kFly];
+                    float sc[kFly];
+#pragma unroll
+                    for (int q = 0; q < kFly; ++q) {
+                        const int c = c0 + q * 32 + lane, col = k * 64 + (c & (row_chunks - 1)) * 8;
+                        if (c >= chunks || col >= m.k1 * 64) continue;
+                        const int t = r.token[m.first + (c >> row_shift)];
+                        if (!w.two) {
+                            v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) + int64_t(t) * a.H + col);
+                        } else {
+                            const uint2 code = __ldg(reinterpret_cast<const uint2*>(
+                                static_cast<const uint8_t*>(a.x) + int64_t(t) * a.H + col));
+                            v[q].x = code.x;
+                            v[q].y = code.y;
+                            sc[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
+                        }
+                    }
+                    if (!ready) {
+                        ready = bar_wait(smem_addr(&empty[0][s]), ((it / w.stages) & 1u) ^ 1u);
+                        if (!ready) { s_failed = 1; break; }
+                    }
+#pragma unroll
+                    for (int q = 0; q < kFly; ++q) {
+                        const int c = c0 + q * 32 + lane, row = c >> row_shift;
+                        const int j = c & (row_chunks - 1);
+                        if (c >= chunks || k * 8 + j >= m.k1 * 8) continue;
+                        uint8_t* sub = tile + (j >> 3) * w.b_sub;
+                        if (w.two) {
+                            uint4 hi, lo;
+                            split_codes(make_uint2(v[q].x, v[q].y), sc[q], hi, lo);
+                            put_chunk(sub, row, j & 7, hi);
+                            put_chunk(sub + part2, row, j & 7, lo);
+                        } else {
+                            put_chunk(sub, row, j & 7, v[q]);
+                        }
+                    }
+                }
+                // each thread orders its writes before the tensor core's reads
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                stop = __any_sync(0xFFFFFFFFu, s_failed != 0);
+                if (stop) break;
+                if (lane == 0) mbar_arrive(smem_addr(&full_b[0][s]));
             }
         }
     } else {
@@ -1003,10 +1031,12 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     static std::atomic<uint64_t> calls{0};
     a.nonce = calls.fetch_add(1, std::memory_order_relaxed) + 1;
 
-    CUtensorMap up, up_small, down;
+    CUtensorMap up, up_small, down, hidden, hidden_big;
     if (!make_map(&up, w_up, a.E * 2 * I, H, kBigBox) ||
         !make_map(&up_small, w_up, a.E * 2 * I, H, kSmallBox) ||
         !make_map(&down, w_down, a.E * H, I, kBigBox) ||
+        !make_map(&hidden, a.hidden, 2 * T * a.k, I, kRowBox) ||
+        !make_map(&hidden_big, a.hidden, 2 * T * a.k, I, kRowBigBox) ||
         !opt_in_smem((const void*)layer_kernel, kSmemBytes))
         return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -1019,7 +1049,7 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, layer_kernel, up, up_small, down, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, layer_kernel, up, up_small, down, hidden, hidden_big, a) != cudaSuccess) {
         cudaGetLastError();                                // not the next call's
         return MOE_ERR_CUDA;
     }
