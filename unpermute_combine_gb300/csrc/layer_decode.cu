@@ -599,6 +599,79 @@ __device__ __forceinline__ void add_up(const LayerArgs& a, const Routing& r, con
             make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
 }
 
+// The up phase's B tiles: the tokens' rows.  Loader warps, teams of w.team of them;
+// a team fills a stage.  kTwo: x is e4m3 codes.
+template <bool kTwo>
+__device__ __forceinline__ void load_tokens(const LayerArgs& a, const Routing& r, const Work& work,
+                                            uint8_t* ring, uint64_t* empty, uint64_t* full,
+                                            volatile int* failed) {
+    const Work w = work;
+    const int lane = int(lane_id()), warp = int(threadIdx.x >> 5) - 2;
+    // No more teams than stages: a warp that waits for a stage has seen the use
+    // before its own last one end, so the stage's barrier can be at most one phase
+    // behind and the parity is not mistaken for an older one.
+    const int mine = warp / w.team, member = warp - mine * w.team;
+    if (mine >= w.teams) return;
+    const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
+    uint32_t it = 0;
+#pragma unroll 1
+    for (int i = blockIdx.x; i < w.items; i += gridDim.x) {
+        const Item m = item_of(w, r, i, true);
+        const int chunks = m.n * row_chunks, part2 = b_rows(m.n, kTwo) * 128;
+#pragma unroll 1
+        for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
+            if (int(it % w.teams) != mine) continue;
+            const int s = it % w.stages, cols = min(w.subs, m.k1 - k) * 8;
+            uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
+            bool ready = false;
+#pragma unroll 1
+            for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
+                // the first chunks (a warp may have none) are loaded before the wait; no
+                // branch around a load, so that all of them are in flight
+                uint4 v[kFly];
+                float sc[kFly];
+#pragma unroll
+                for (int q = 0; q < kFly; ++q) {
+                    const int c = min(c0 + q * 32 + lane, chunks - 1);
+                    const int j = min(c & (row_chunks - 1), cols - 1);
+                    const int t = r.token[m.first + (c >> row_shift)], col = k * 64 + j * 8;
+                    if constexpr (kTwo) {
+                        const uint2 code = __ldg(reinterpret_cast<const uint2*>(
+                            static_cast<const uint8_t*>(a.x) + int64_t(t) * a.H + col));
+                        v[q].x = code.x;
+                        v[q].y = code.y;
+                        sc[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
+                    } else {
+                        v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) + int64_t(t) * a.H + col);
+                    }
+                }
+                if (!ready) {
+                    ready = bar_wait(smem_addr(&empty[s]), ((it / w.stages) & 1u) ^ 1u);
+                    if (!ready) { *failed = 1; break; }
+                }
+#pragma unroll
+                for (int q = 0; q < kFly; ++q) {
+                    const int c = c0 + q * 32 + lane, row = c >> row_shift, j = c & (row_chunks - 1);
+                    if (c >= chunks || j >= cols) continue;
+                    uint8_t* sub = tile + (j >> 3) * w.b_sub;
+                    if constexpr (kTwo) {
+                        uint4 hi, lo;
+                        split_codes(make_uint2(v[q].x, v[q].y), sc[q], hi, lo);
+                        put_chunk(sub, row, j & 7, hi);
+                        put_chunk(sub + part2, row, j & 7, lo);
+                    } else {
+                        put_chunk(sub, row, j & 7, v[q]);
+                    }
+                }
+            }
+            // each thread orders its writes before the tensor core's reads
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (__any_sync(0xFFFFFFFFu, *failed != 0)) return;
+            if (lane == 0) mbar_arrive(smem_addr(&full[s]));
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_up_small,
              const __grid_constant__ CUtensorMap map_down, const __grid_constant__ CUtensorMap map_hidden,
@@ -814,71 +887,10 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         }
     } else if (warp < 2 + kLoaders) {
         // -------------------------------------------------- B loaders, up phase
-        const Work w = s_work[0];
-        // No more teams than stages: a warp that waits for a stage has seen the use
-        // before its own last one end, so the stage's barrier can be at most one phase
-        // behind and the parity is not mistaken for an older one.
-        const int mine = (warp - 2) / w.team, member = (warp - 2) - mine * w.team;
-        const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
-        uint32_t it = 0;
-        bool stop = mine >= w.teams;                       // the same in all lanes
-#pragma unroll 1
-        for (int i = blockIdx.x; i < w.items && !stop; i += gridDim.x) {
-            const Item m = item_of(w, r, i, true);
-            const int chunks = m.n * row_chunks, part2 = b_rows(m.n, w.two) * 128;
-#pragma unroll 1
-            for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
-                if (int(it % w.teams) != mine) continue;
-                const int s = it % w.stages;
-                uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
-                bool ready = false;
-#pragma unroll 1
-                for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
-                    // the first chunks (a warp may have none) are loaded before the wait
-                    uint4 v[kFly];
-                    float sc[kFly];
-#pragma unroll
-                    for (int q = 0; q < kFly; ++q) {
-                        const int c = c0 + q * 32 + lane, col = k * 64 + (c & (row_chunks - 1)) * 8;
-                        if (c >= chunks || col >= m.k1 * 64) continue;
-                        const int t = r.token[m.first + (c >> row_shift)];
-                        if (!w.two) {
-                            v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) + int64_t(t) * a.H + col);
-                        } else {
-                            const uint2 code = __ldg(reinterpret_cast<const uint2*>(
-                                static_cast<const uint8_t*>(a.x) + int64_t(t) * a.H + col));
-                            v[q].x = code.x;
-                            v[q].y = code.y;
-                            sc[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
-                        }
-                    }
-                    if (!ready) {
-                        ready = bar_wait(smem_addr(&empty[0][s]), ((it / w.stages) & 1u) ^ 1u);
-                        if (!ready) { s_failed = 1; break; }
-                    }
-#pragma unroll
-                    for (int q = 0; q < kFly; ++q) {
-                        const int c = c0 + q * 32 + lane, row = c >> row_shift;
-                        const int j = c & (row_chunks - 1);
-                        if (c >= chunks || k * 8 + j >= m.k1 * 8) continue;
-                        uint8_t* sub = tile + (j >> 3) * w.b_sub;
-                        if (w.two) {
-                            uint4 hi, lo;
-                            split_codes(make_uint2(v[q].x, v[q].y), sc[q], hi, lo);
-                            put_chunk(sub, row, j & 7, hi);
-                            put_chunk(sub + part2, row, j & 7, lo);
-                        } else {
-                            put_chunk(sub, row, j & 7, v[q]);
-                        }
-                    }
-                }
-                // each thread orders its writes before the tensor core's reads
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                stop = __any_sync(0xFFFFFFFFu, s_failed != 0);
-                if (stop) break;
-                if (lane == 0) mbar_arrive(smem_addr(&full_b[0][s]));
-            }
-        }
+        if (s_work[0].two)
+            load_tokens<true>(a, r, s_work[0], ring, empty[0], full_b[0], &s_failed);
+        else
+            load_tokens<false>(a, r, s_work[0], ring, empty[0], full_b[0], &s_failed);
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3, row = q * 32 + lane;       // TMEM lane quadrant, tile row
