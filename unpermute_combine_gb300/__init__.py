@@ -202,6 +202,8 @@ def _workspace(nbytes, like, given):
 # fastest, and pointers are passed as integers.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_Tensor = torch.Tensor
 
 
 class _Target:
@@ -212,22 +214,20 @@ class _Target:
     __slots__ = ("device", "where", "stream", "handle")
 
     def __init__(self, stream, like, name):
-        if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        if not isinstance(like, _Tensor) or not like.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        self.device = like.get_device()
-        if self.device != torch.cuda.current_device():
-            raise ValueError(f"{name} is on cuda:{self.device}, but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+        self.device = device = like.get_device()
+        if device != _current_device():
+            raise ValueError(f"{name} is on cuda:{device}, but the current device is "
+                             f"cuda:{_current_device()}")
         self.where = like.device
         self.stream = stream
-        self.handle = _raw_stream(self.device) if stream is None else stream.cuda_stream
+        self.handle = _raw_stream(device) if stream is None else stream.cuda_stream
 
     def given(self, t, name, dtype, shape=None):
         """The address of a caller's tensor, checked."""
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.get_device() != self.device:
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{self.device}")
+        if not isinstance(t, _Tensor) or t.get_device() != self.device:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{self.device}")
         if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if shape is not None and t.shape != shape:
@@ -873,13 +873,13 @@ def moe_grouped_swiglu_wgrad(x: torch.Tensor, hidden: torch.Tensor, dy: torch.Te
 
 def _norm_rows(t, x, name, weight):
     """(dtype codes of x [T,H] and weight [H], their addresses)."""
-    dtype, wdtype = x.dtype, weight.dtype if isinstance(weight, torch.Tensor) else None
-    if x.dim() != 2 or dtype not in _DT:
-        raise ValueError(f"{name} must be float32 or bfloat16 [T, H], got {dtype} with {x.dim()} dims")
-    if wdtype not in _DT:
-        raise ValueError(f"weight must be float32 or bfloat16, got {wdtype}")
-    return (_DT[dtype], _DT[wdtype], t.given(x, name, dtype),
-            t.given(weight, "weight", wdtype, x.shape[1:]))
+    dt, wdt = _DT.get(x.dtype), _DT.get(weight.dtype) if isinstance(weight, _Tensor) else None
+    if dt is None or x.dim() != 2:
+        raise ValueError(f"{name} must be float32 or bfloat16 [T, H], got {x.dtype} with "
+                         f"{x.dim()} dims")
+    if wdt is None:
+        raise ValueError("weight must be float32 or bfloat16")
+    return dt, wdt, t.given(x, name, x.dtype), t.given(weight, "weight", weight.dtype, x.shape[1:])
 
 
 def _norm_residual(t, x, residual, residual_out):
