@@ -484,8 +484,9 @@ moe_status_t moe_permute_quantize_fp8(const void* x, int64_t T, int64_t H, int b
  *   x, residual, residual_out, out [T,H] (dtype: MOE_F32 or MOE_BF16);
  *   weight [H] (weight_dtype: MOE_F32 or MOE_BF16); eps >= 0.
  * residual_out and out may each be x or residual itself (the stream updated in
- * place), but not one another; no other overlap.  Any H and alignment; H a
- * multiple of 8 with 16-byte aligned pointers takes the vectorised path.
+ * place), but not one another (else MOE_ERR_INVALID_ARG); no other overlap.
+ * Any H and alignment; tensors that start on 16-byte boundaries take the
+ * vectorised paths.
  *
  * moe_rmsnorm_quantize_fp8: the same norm with the output quantized as
  * moe_quantize_fp8 does, from the float32 values (not from bf16 ones): per
@@ -514,7 +515,9 @@ moe_status_t moe_rmsnorm_quantize_fp8(const void* x, const void* residual, moe_d
  *   completely (zeros for T = 0), in an order that only T, H and the
  *   alignment decide.
  * grad_x may be grad_y, grad_h or h itself; no other overlap.  Workspace:
- * moe_rmsnorm_backward_workspace_size(T, H) bytes, which may hold anything. */
+ * moe_rmsnorm_backward_workspace_size(T, H) bytes, which may hold anything.
+ * Rows in memory that starts on 16-byte boundaries come by bulk copies; a
+ * bounded wait there that gives up is reported by moe_device_status. */
 moe_status_t moe_rmsnorm_backward_workspace_size(int64_t T, int64_t H, size_t* bytes);
 
 moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const void* h,

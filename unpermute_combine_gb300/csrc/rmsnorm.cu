@@ -435,6 +435,11 @@ __host__ __device__ constexpr uint32_t slot_size(int64_t H, bool three) {
 // thread.  The columns' shares of grad_weight stay in registers over all rows of
 // the block; its teams' shares are added up at the end, in order, and the blocks'
 // by rmsnorm_grad_weight_kernel.
+// Bound by memory on long batches (16384 rows of 7168 in bf16 with grad_h: 145 us,
+// 6.5 TB/s), by the way in and out of the ring on short ones (4096 rows of 2048, 3.4
+// rows a team: 22 us with the second launch, of which 10 move the bytes).  One row a
+// block at a time, without a ring: 295 and 44 us.  Packed float instructions and
+// fewer shuffles: no faster, though 70% of the issue slots are taken.
 template <typename X, typename W, int V, bool kShift>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
