@@ -486,7 +486,7 @@ moe_status_t moe_permute_quantize_fp8(const void* x, int64_t T, int64_t H, int b
  * residual_out and out may each be x or residual itself (the stream updated in
  * place), but not one another (else MOE_ERR_INVALID_ARG); no other overlap.
  * Any H and alignment; tensors that start on 16-byte boundaries take the
- * vectorised paths.
+ * vectorised paths; one off its elements' boundaries is MOE_ERR_INVALID_ARG.
  *
  * moe_rmsnorm_quantize_fp8: the same norm with the output quantized as
  * moe_quantize_fp8 does, from the float32 values (not from bf16 ones): per
@@ -549,8 +549,8 @@ moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const 
  * [T, H/128] float (block = 128, as moe_rmsnorm_quantize_fp8 and
  * moe_quantize_fp8 leave them), standing for code * scale.
  * w_up_packed [E,2I,H], w_down_packed [E,H,I]: moe_grouped_swiglu_pack's.
- * Shapes: T <= 64, H a multiple of 256, I of 128, 1 <= k <= min(E, 32),
- * E <= 1024 (else MOE_ERR_UNSUPPORTED); x, weights and out 16-byte aligned
+ * Shapes: T <= 64, H a multiple of 256, I of 128, both at most 2^20, 1 <= k <=
+ * min(E, 32), E <= 1024 (else MOE_ERR_UNSUPPORTED); x, weights and out 16-byte aligned
  * (else MOE_ERR_INVALID_ARG).  out must not overlap x.  Workspace:
  * moe_layer_decode_workspace_size bytes, which may hold anything; calls that
  * share one must not overlap on the GPU. */

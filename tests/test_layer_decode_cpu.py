@@ -36,7 +36,8 @@ def test_refusals(lib, call):
                dict(x=P(0x2000), out=P(0x2000))):
         assert call(lib, **kw) == INVALID, kw
     for kw in (dict(T=65), dict(E=1025, k=2), dict(k=9), dict(E=64, k=33), dict(H=128), dict(H=300),
-               dict(I=64), dict(I=130), dict(E=1024, I=1 << 20)):
+               dict(I=64), dict(I=130), dict(E=1024, I=1 << 20),
+               dict(E=1, k=1, H=1 << 21), dict(E=1, k=1, I=1 << 21)):
         assert call(lib, **kw) == UNSUPPORTED, kw
     n = moe.moe_layer_decode_workspace_size(4, 8, 2, 256, 128)
     assert call(lib, n=n - 1) == WORKSPACE

@@ -48,6 +48,16 @@ def test_norm(lib):
     assert norm(lib, x=None, w=None, out=None, H=0) == OK
 
 
+def test_elements_off_their_boundaries(lib):
+    odd, half = P(0x1001), P(0x1002)
+    for kw in (dict(x=odd), dict(w=odd), dict(out=odd), dict(res=odd, ho=fake), dict(res=half, ho=odd),
+               dict(x=half, dt=0), dict(out=half, dt=0), dict(w=half, wdt=0)):
+        assert norm(lib, **{**dict(out=P(0x8000)), **kw}) == INVALID, kw
+    for kw in (dict(g=odd), dict(h=odd), dict(gx=odd), dict(gh=odd), dict(w=odd), dict(gw=half),
+               dict(g=half, dt=0), dict(w=half, wdt=0)):
+        assert back(lib, **kw) == INVALID, kw
+
+
 def test_quantize(lib):
     assert quant(lib, q=None) == INVALID and quant(lib, sc=None) == INVALID
     assert quant(lib, res=fake) == INVALID

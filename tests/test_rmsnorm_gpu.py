@@ -131,6 +131,35 @@ def test_norm_of_unaligned_rows(off, dtype):
     assert (np.abs(_val(y) - y64) <= ((_depth(H) / 2 + 8) * U + HALF[dtype]) * np.abs(y64)).all()
 
 
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 1), (9, 3), (5, 7), (20, 5), (6, 13), (2, 1001), (40, 33)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_between_others(T, H, dtype):
+    """What lies before and behind the tensors, NaN here, is neither used nor
+    changed, forward and backward; rows shorter than a chunk among them."""
+    x, res, w = _inputs(T, H, dtype, dtype, True, T * 5 + H)
+
+    def between(a):
+        t = to_dev(a) if a is not None else torch.zeros((T, H), dtype=to_dev(x).dtype, device="cuda")
+        big = torch.full((64 + t.numel() + 64,), float("nan"), dtype=t.dtype, device="cuda")
+        big[64:64 + t.numel()] = t.view(-1)
+        return big, big[64:64 + t.numel()].view(t.shape)
+    bufs = [between(a) for a in (x, res, None, None, None)]
+    (_, xd), (_, rd), (_, ho), (_, out), (_, gx) = bufs
+    wd = to_dev(w)
+    y, h = moe.moe_rmsnorm(xd, wd, residual=rd, out=out, residual_out=ho)
+    h_o = _sum(x, res)
+    assert (to_host(h) == h_o).all()
+    y64, _ = _norm64(h_o, w, 1e-6)
+    assert (np.abs(_val(y) - y64) <= ((_depth(H) / 2 + 8) * U + HALF[dtype]) * np.abs(y64)).all()
+    g, gw = moe.moe_rmsnorm_backward(xd, h, wd, grad_h=rd, grad_x=gx)
+    gx64, size, gw64, gw_size = _backward64(x, h_o, w, res, 1e-6)
+    D = _depth(H)
+    assert (np.abs(_val(g) - gx64) <= (2.5 * D + 24) * U * size + HALF[dtype] * np.abs(gx64)).all()
+    assert (np.abs(_val(gw) - gw64) <= (D / 2 + 10 + T) * U * gw_size).all()
+    for big, t in bufs:
+        assert torch.isnan(big[:64]).all() and torch.isnan(big[64 + t.numel():]).all()
+
+
 def test_norm_leaves_what_lies_behind():
     T, H = 5, 333
     x, res, w = _inputs(T, H, "bf16", "f32", True, 3)

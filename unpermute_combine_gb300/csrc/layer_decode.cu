@@ -50,6 +50,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxTokens = 64;
+constexpr int kMaxSize = 1 << 20;         // of H and I
 constexpr int kM = 128;                   // rows of an MMA, weight rows of a down tile
 constexpr int kBigBox = 64, kSmallBox = 16;    // weight rows of a TMA box
 constexpr int kRowBox = 8, kRowBigBox = 32;    // hidden rows of one
@@ -996,6 +997,7 @@ moe_status_t check_layer(int64_t T, int E, int k, int64_t H, int64_t I) {
     if (T < 0 || E < 1 || k < 1 || H < 1 || I < 1) return MOE_ERR_INVALID_ARG;
     if (T > kMaxTokens || E > kMaxExperts || k > kMaxTopK || k > E || H % 256 != 0 || I % 128 != 0)
         return MOE_ERR_UNSUPPORTED;
+    if (H > kMaxSize || I > kMaxSize) return MOE_ERR_UNSUPPORTED;    // (int arithmetic below)
     if (int64_t(E) * 2 * I >= (int64_t(1) << 31) || int64_t(E) * H >= (int64_t(1) << 31))
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;

@@ -113,11 +113,12 @@ __device__ __forceinline__ int row_shift(int64_t row, int64_t H) {
 }
 
 // The chunk from element p on.  Elements of the rows next to this one come along
-// (clear_others takes them out), but nothing past the tensor's last row is read.
+// (clear_others takes them out), but nothing past the tensor's end, `left` elements
+// from the row's start, is read.
 template <bool kShift, typename X>
-__device__ __forceinline__ Raw<X> load_at(const X* row, int p, int H, bool last) {
+__device__ __forceinline__ Raw<X> load_at(const X* row, int p, int H, int64_t left) {
     if constexpr (kShift) {
-        if (last && p + kChunk > H) {
+        if (p + kChunk > left) {
             float f[kChunk];
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) f[i] = p + i >= 0 && p + i < H ? load1(row + p + i) : 0.0f;
@@ -232,12 +233,13 @@ rmsnorm_kernel(const NormArgs a) {
         const X* x = static_cast<const X*>(a.x) + row * a.H;
         const int shift = kShift ? row_shift<X>(row, a.H) : 0;
         const int chunks = (H + shift + kChunk - 1) / kChunk;
+        const int64_t left = (a.T - row) * a.H;
         Raw<X> h[V];
         float ss = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
-            if (c < chunks) h[v] = load_at<kShift>(x, c * kChunk - shift, H, row == a.T - 1);
+            if (c < chunks) h[v] = load_at<kShift>(x, c * kChunk - shift, H, left);
         }
         if (a.residual) {
             const X* res = static_cast<const X*>(a.residual) + row * a.H;
@@ -246,7 +248,7 @@ rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = threadIdx.x + v * blockDim.x;
-                if (c < chunks) add[v] = load_at<kShift>(res, c * kChunk - shift, H, row == a.T - 1);
+                if (c < chunks) add[v] = load_at<kShift>(res, c * kChunk - shift, H, left);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -754,6 +756,14 @@ int row_chunks(int64_t H) {
 // Rows of at most kMaxThreads * kChunk elements are held by threads of eight.
 bool odd_fits(int64_t H) { return H <= int64_t(kMaxThreads) * kChunk; }
 
+// Whether every pointer is on a boundary of its element.
+bool on_elements(int dtype, std::initializer_list<const void*> ptrs) {
+    const uintptr_t low = elem_size(moe_dtype_t(dtype)) - 1;
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) & low) return false;
+    return true;
+}
+
 // How a call's rows lie: on 16-byte boundaries, in memory that starts on one, or not.
 enum Rows : int { kVectors, kShifted, kElements };
 
@@ -878,6 +888,8 @@ extern "C" moe_status_t moe_rmsnorm(const void* x, const void* residual, moe_dty
     if (!x || !weight || !out || (residual && (!residual_out || residual_out == out)))
         return MOE_ERR_INVALID_ARG;
     if (!residual) residual_out = nullptr;
+    if (!on_elements(dtype, {x, residual, residual_out, out}) || !on_elements(weight_dtype, {weight}))
+        return MOE_ERR_INVALID_ARG;
     const NormArgs a{x, residual, weight, residual_out, out, nullptr, T, H, eps, 0};
     const Rows how = rows_of(H, weight, {x, residual, residual_out, out});
     return dispatch_norm<false>(a, dtype, weight_dtype, how, static_cast<cudaStream_t>(stream));
@@ -922,12 +934,14 @@ extern "C" moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* gra
     const moe_status_t st = check_norm(dtype, weight_dtype, T, H, eps);
     if (st != MOE_OK) return st;
     if (H == 0) return MOE_OK;
-    if (!grad_weight) return MOE_ERR_INVALID_ARG;
+    if (!grad_weight || !on_elements(MOE_F32, {grad_weight})) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0)
         return cudaMemsetAsync(grad_weight, 0, size_t(H) * 4, s) == cudaSuccess ? MOE_OK
                                                                                : MOE_ERR_CUDA;
     if (!grad_y || !h || !weight || !grad_x) return MOE_ERR_INVALID_ARG;
+    if (!on_elements(dtype, {grad_y, grad_h, h, grad_x}) || !on_elements(weight_dtype, {weight}))
+        return MOE_ERR_INVALID_ARG;
     size_t need = 0;
     const moe_status_t sz = moe_rmsnorm_backward_workspace_size(T, H, &need);
     if (sz != MOE_OK) return sz;
