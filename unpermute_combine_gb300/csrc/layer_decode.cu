@@ -52,7 +52,6 @@ namespace {
 constexpr int kMaxTokens = 64;
 constexpr int kMaxSize = 1 << 20;         // of H and I
 constexpr int kM = 128;                   // rows of an MMA, weight rows of a down tile
-constexpr int kBigBox = 64, kSmallBox = 16;    // weight rows of a TMA box
 constexpr int kRowBox = 8, kRowBigBox = 32;    // hidden rows of one
 constexpr int kMaxStages = 16;
 constexpr int kLoaders = 9;               // warps that fill B tiles
@@ -674,7 +673,8 @@ __device__ __forceinline__ void load_tokens(const LayerArgs& a, const Routing& r
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_up_small,
+layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__ CUtensorMap map_up32,
+             const __grid_constant__ CUtensorMap map_up16,
              const __grid_constant__ CUtensorMap map_down, const __grid_constant__ CUtensorMap map_hidden,
              const __grid_constant__ CUtensorMap map_hidden_big, const LayerArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -711,7 +711,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     } else if (warp == 1) {
         if (lane == 0) {
             prefetch_map(&map_up);
-            prefetch_map(&map_up_small);
+            prefetch_map(&map_up32);
+            prefetch_map(&map_up16);
             prefetch_map(&map_down);
             prefetch_map(&map_hidden);
             prefetch_map(&map_hidden_big);
@@ -758,17 +759,14 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                     const int row = up ? m.e * 2 * a.I + m.col / 128 * 256 + m.col % 128
                                        : m.e * a.H + m.strip * kM;
                     const int row2 = row + (up ? 128 : kM / 2), half = m.cols;
-                    const int box = half == kBigBox ? kBigBox : kSmallBox;
-                    const CUtensorMap* map = !up ? &map_down : half == kBigBox ? &map_up : &map_up_small;
+                    const CUtensorMap* map = !up ? &map_down : half == 64 ? &map_up
+                                             : half == 32 ? &map_up32 : &map_up16;
 #pragma unroll 1
                     for (int u = 0; u < min(w.subs, m.k1 - k); ++u) {
                         const int c = (k + u) * 64;
                         const uint32_t to = dst + u * w.a_sub;
-#pragma unroll 1
-                        for (int b = 0; b < half; b += box) {
-                            tma_load_2d_hint(to + b * 128, map, c, row + b, bar, once);
-                            tma_load_2d_hint(to + (half + b) * 128, map, c, row2 + b, bar, once);
-                        }
+                        tma_load_2d_hint(to, map, c, row, bar, once);
+                        tma_load_2d_hint(to + half * 128, map, c, row2, bar, once);
                     }
                 };
                 uint32_t it = 0;
@@ -1045,10 +1043,10 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     static std::atomic<uint64_t> calls{0};
     a.nonce = calls.fetch_add(1, std::memory_order_relaxed) + 1;
 
-    CUtensorMap up, up_small, down, hidden, hidden_big;
-    if (!make_map(&up, w_up, a.E * 2 * I, H, kBigBox) ||
-        !make_map(&up_small, w_up, a.E * 2 * I, H, kSmallBox) ||
-        !make_map(&down, w_down, a.E * H, I, kBigBox) ||
+    // boxes of half a tile's rows
+    CUtensorMap up, up32, up16, down, hidden, hidden_big;
+    if (!make_map(&up, w_up, a.E * 2 * I, H, 64) || !make_map(&up32, w_up, a.E * 2 * I, H, 32) ||
+        !make_map(&up16, w_up, a.E * 2 * I, H, 16) || !make_map(&down, w_down, a.E * H, I, kM / 2) ||
         !make_map(&hidden, a.hidden, 2 * T * a.k, I, kRowBox) ||
         !make_map(&hidden_big, a.hidden, 2 * T * a.k, I, kRowBigBox) ||
         !opt_in_smem((const void*)layer_kernel, kSmemBytes))
@@ -1063,7 +1061,7 @@ moe_status_t layer(LayerArgs a, const void* w_up, const void* w_down, int64_t T,
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, layer_kernel, up, up_small, down, hidden, hidden_big, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, layer_kernel, up, up32, up16, down, hidden, hidden_big, a) != cudaSuccess) {
         cudaGetLastError();                                // not the next call's
         return MOE_ERR_CUDA;
     }
