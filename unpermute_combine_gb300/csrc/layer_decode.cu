@@ -797,7 +797,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------------ MMA issuer
             uint32_t tile = 0;
 #pragma unroll 1

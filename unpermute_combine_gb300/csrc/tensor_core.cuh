@@ -64,6 +64,17 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
            (uint32_t(m >> 4) << 24);
 }
 
+// One of a whole warp's threads.  A branch on it, unlike one on the lane, lets the compiler know that
+// one thread alone runs what follows: the decode layer's MMAs, which took 116 to 140 cycles each to
+// issue behind a test of the lane, are no longer what its narrow tiles wait for.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
     asm volatile(
