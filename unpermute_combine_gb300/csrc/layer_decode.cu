@@ -745,7 +745,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     // Every role: the up phase, then the down phase.  Items of a phase go to the
     // blocks in turn.
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ---------------------------------------------------- TMA producer
             // weights leave L2 before what every call needs again
             const uint64_t once = policy_evict_first();
@@ -847,7 +847,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     } else if (warp == kEpilogue - 1) {
         // ------------------------------ waits for the other blocks; B tiles, down phase
         if (!wait_for_blocks(a, 0, s_token)) s_failed = 1;
-        if (lane == 0) {
+        if (elect_one()) {
             // the hidden rows, which other blocks' threads wrote and copies now read
             asm volatile("fence.proxy.async;" ::: "memory");
             const Work w = s_work[1];
