@@ -599,6 +599,67 @@ __device__ __forceinline__ void add_up(const LayerArgs& a, const Routing& r, con
             make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
 }
 
+// Starts the copy of chunk c of a row of a B tile.
+__device__ __forceinline__ void copy_chunk(uint8_t* tile, int row, int c, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(smem_addr(tile + row * 128 + ((c ^ (row & 7)) << 4))), "l"(from) : "memory");
+}
+
+// A stage's B tiles from rows of bf16, chunks of 16 bytes: asynchronous copies, all of
+// them in flight at once (through registers, 8 at a time: 64 tokens of 8 experts of 4096
+// by 2048, 108 us against 97).  Wants 16 bytes of alignment, which x has.
+__device__ __forceinline__ void load_stage(const LayerArgs& a, const Routing& r, const Work& w,
+                                           const Item& m, int k, int cols, int member, uint8_t* tile) {
+    const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift, chunks = m.n * row_chunks;
+#pragma unroll 4
+    for (int c = member * 32 + int(lane_id()); c < chunks; c += w.team * 32) {
+        const int row = c >> row_shift, j = c & (row_chunks - 1);
+        if (j >= cols) continue;
+        const int64_t at = int64_t(r.token[m.first + row]) * a.H + k * 64 + j * 8;
+        copy_chunk(tile + (j >> 3) * w.b_sub, row, j & 7, static_cast<const uint16_t*>(a.x) + at);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The same from e4m3 codes and their scales, chunks of 8 codes, as values in two parts.
+// Loads what comes first before it waits for the stage; false: the wait ran out.
+__device__ __forceinline__ bool load_codes(const LayerArgs& a, const Routing& r, const Work& w,
+                                           const Item& m, int k, int cols, int member, uint8_t* tile,
+                                           uint32_t empty, uint32_t parity) {
+    const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift, chunks = m.n * row_chunks;
+    const int part2 = b_rows(m.n, true) * 128;
+    bool ready = false;
+#pragma unroll 1
+    for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
+        // (a warp may have no chunk) no branch around a load, so that all of them are in
+        // flight
+        uint2 code[kFly];
+        float scale[kFly];
+#pragma unroll
+        for (int q = 0; q < kFly; ++q) {
+            const int c = min(c0 + q * 32 + int(lane_id()), chunks - 1);
+            const int j = min(c & (row_chunks - 1), cols - 1);
+            const int t = r.token[m.first + (c >> row_shift)], col = k * 64 + j * 8;
+            code[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) +
+                                                           int64_t(t) * a.H + col));
+            scale[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
+        }
+        if (!ready) ready = bar_wait(empty, parity);
+        if (!ready) return false;
+#pragma unroll
+        for (int q = 0; q < kFly; ++q) {
+            const int c = c0 + q * 32 + int(lane_id()), row = c >> row_shift, j = c & (row_chunks - 1);
+            if (c >= chunks || j >= cols) continue;
+            uint8_t* sub = tile + (j >> 3) * w.b_sub;
+            uint4 hi, lo;
+            split_codes(code[q], scale[q], hi, lo);
+            put_chunk(sub, row, j & 7, hi);
+            put_chunk(sub + part2, row, j & 7, lo);
+        }
+    }
+    return true;
+}
+
 // The up phase's B tiles: the tokens' rows.  Loader warps, teams of w.team of them;
 // a team fills a stage.  kTwo: x is e4m3 codes.
 template <bool kTwo>
@@ -612,57 +673,21 @@ __device__ __forceinline__ void load_tokens(const LayerArgs& a, const Routing& r
     // behind and the parity is not mistaken for an older one.
     const int mine = warp / w.team, member = warp - mine * w.team;
     if (mine >= w.teams) return;
-    const int row_chunks = 8 * w.subs, row_shift = 3 + w.shift;
     uint32_t it = 0;
 #pragma unroll 1
     for (int i = blockIdx.x; i < w.items; i += gridDim.x) {
         const Item m = item_of(w, r, i, true);
-        const int chunks = m.n * row_chunks, part2 = b_rows(m.n, kTwo) * 128;
 #pragma unroll 1
         for (int k = m.k0; k < m.k1; k += w.subs, ++it) {
             if (int(it % w.teams) != mine) continue;
             const int s = it % w.stages, cols = min(w.subs, m.k1 - k) * 8;
+            const uint32_t bar = smem_addr(&empty[s]), parity = ((it / w.stages) & 1u) ^ 1u;
             uint8_t* tile = ring + s * w.stage_bytes + w.subs * w.a_sub;
-            bool ready = false;
-#pragma unroll 1
-            for (int c0 = member * 32 * kFly; c0 < chunks || !ready; c0 += w.team * 32 * kFly) {
-                // the first chunks (a warp may have none) are loaded before the wait; no
-                // branch around a load, so that all of them are in flight
-                uint4 v[kFly];
-                float sc[kFly];
-#pragma unroll
-                for (int q = 0; q < kFly; ++q) {
-                    const int c = min(c0 + q * 32 + lane, chunks - 1);
-                    const int j = min(c & (row_chunks - 1), cols - 1);
-                    const int t = r.token[m.first + (c >> row_shift)], col = k * 64 + j * 8;
-                    if constexpr (kTwo) {
-                        const uint2 code = __ldg(reinterpret_cast<const uint2*>(
-                            static_cast<const uint8_t*>(a.x) + int64_t(t) * a.H + col));
-                        v[q].x = code.x;
-                        v[q].y = code.y;
-                        sc[q] = __ldg(a.x_scales + int64_t(t) * (a.H / 128) + col / 128);
-                    } else {
-                        v[q] = ld_nc_v4(static_cast<const uint16_t*>(a.x) + int64_t(t) * a.H + col);
-                    }
-                }
-                if (!ready) {
-                    ready = bar_wait(smem_addr(&empty[s]), ((it / w.stages) & 1u) ^ 1u);
-                    if (!ready) { *failed = 1; break; }
-                }
-#pragma unroll
-                for (int q = 0; q < kFly; ++q) {
-                    const int c = c0 + q * 32 + lane, row = c >> row_shift, j = c & (row_chunks - 1);
-                    if (c >= chunks || j >= cols) continue;
-                    uint8_t* sub = tile + (j >> 3) * w.b_sub;
-                    if constexpr (kTwo) {
-                        uint4 hi, lo;
-                        split_codes(make_uint2(v[q].x, v[q].y), sc[q], hi, lo);
-                        put_chunk(sub, row, j & 7, hi);
-                        put_chunk(sub + part2, row, j & 7, lo);
-                    } else {
-                        put_chunk(sub, row, j & 7, v[q]);
-                    }
-                }
+            if constexpr (kTwo) {
+                if (!load_codes(a, r, w, m, k, cols, member, tile, bar, parity)) *failed = 1;
+            } else {
+                if (bar_wait(bar, parity)) load_stage(a, r, w, m, k, cols, member, tile);
+                else *failed = 1;
             }
             // each thread orders its writes before the tensor core's reads
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
