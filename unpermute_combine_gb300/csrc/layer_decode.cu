@@ -59,8 +59,8 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kEpilogue = 3 + kLoaders;   // its first warp
 static_assert(kEpilogue + 4 == kWarps && kEpilogue % 4 == 0, "warp roles");
 constexpr int kFly = 8;                   // chunks that a loader's lane has in flight
-constexpr int kExchBytes = 8 * 64 * 4;    // up values on their way to the gate's threads
-constexpr int kSmemBytes = 224 * 1024;    // dynamic shared memory of a block, one on an SM
+constexpr int kExchBytes = 2 * 8 * 64 * 4;    // gate and up values on their way to each other
+constexpr int kSmemBytes = 226 * 1024;    // dynamic shared memory of a block, one on an SM
 constexpr int kMaxParts = 8;              // parts of a down tile's K
 constexpr uint32_t kTmemCols = 256;       // two accumulators of up to 128 columns
 // Most blocks of a launch, whatever the GPU.
@@ -716,7 +716,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     const int ring_bytes = kSmemBytes - 1024 - kExchBytes - int(routing_bytes(a.T, a.E, a.k));
-    float* exch = reinterpret_cast<float*>(ring + ring_bytes);                 // [8][64]
+    float* exch = reinterpret_cast<float*>(ring + ring_bytes);                 // [2][8][64]
     const Routing r = carve_routing(ring + ring_bytes + kExchBytes, a.T, a.E, a.k);
 
     // the tokens' rows, on their way to L2 while the routing is worked out
@@ -943,26 +943,34 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                         for (int c = 0; c < 8; ++c) v[c] += lo[c];
                     }
                     if (up) {
-                        // the tile's first rows hold the gate, the next ones the up values
-                        if (row >= m.cols && row < 2 * m.cols) {
+                        // The tile's first rows hold the gate, the next ones the up values.  A
+                        // gate's thread works on the first 4 tokens, an up value's on the others;
+                        // the threads of every other 8 tokens have the same half of `exch`.
+                        const bool gate = row < m.cols;
+                        const int col = gate ? row : row - m.cols, c1 = gate ? 0 : 4;
+                        float* ex = exch + (c0 & 8) * 64 + col;
+                        if (col < m.cols) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) exch[c * 64 + row - m.cols] = v[c];
+                            for (int c = 0; c < 4; ++c) ex[(4 - c1 + c) * 64] = gate ? v[4 + c] : v[c];
                         }
                         bar_epilogue();
-                        if (row < m.cols) {
-                            uint16_t* hp = a.hidden + int64_t(m.first + c0) * a.I + m.col + row;
+                        if (col < m.cols) {
+                            uint16_t* hp = a.hidden + int64_t(m.first + c0 + c1) * a.I + m.col + col;
+                            float h[4];
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                if (c0 + c >= m.n) break;
-                                const float h = __fdividef(v[c], 1.0f + __expf(-v[c])) *
-                                                exch[c * 64 + row];
-                                const uint16_t hi = f32_to_bf16_rn(h);
+                            for (int c = 0; c < 4; ++c) {
+                                const float other = ex[(c1 + c) * 64], g = gate ? v[c] : other;
+                                h[c] = __fdividef(g, 1.0f + __expf(-g)) * (gate ? other : v[4 + c]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                if (c0 + c1 + c >= m.n) continue;
+                                const uint16_t hi = f32_to_bf16_rn(h[c]);
                                 hp[int64_t(c) * a.I] = hi;
                                 hp[(int64_t(a.T) * a.k + c) * a.I] =
-                                    f32_to_bf16_rn(bf16_rest(h, bf16_to_f32(hi)));
+                                    f32_to_bf16_rn(bf16_rest(h[c], bf16_to_f32(hi)));
                             }
                         }
-                        bar_epilogue();
                     } else {
                         float* yp = a.y + m.strip * kM + row;
                         float* pp = a.parts + (int64_t(m.cut) * min(w.group, a.T) + c0) * kM + row;
