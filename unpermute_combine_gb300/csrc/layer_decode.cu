@@ -13,19 +13,22 @@
 //   warp 0        TMA producer: stages of weight rows x up to 256 of K, in a
 //                 ring that fills the SM's shared memory
 //   warp 1        one thread issues the MMAs
-//   warps 2..10   fill the up phase's B tiles with gathered token rows (e4m3 codes
-//                 times their scale), one or several warps a stage, so that the
-//                 latency of several gathers overlaps (warp 2 also has the tensor
-//                 memory)
+//   warps 2..10   fill the up phase's B tiles with gathered token rows (asynchronous
+//                 copies; e4m3 codes times their scale through registers), one or
+//                 several warps a stage, so that the latency of several gathers
+//                 overlaps (warp 2 also has the tensor memory)
 //   warp 11       waits for the other blocks, and copies hidden rows into the down
 //                 phase's B tiles
 //   warps 12..15  epilogue: silu(gate) * up, or the down products
+// The issuing threads are elected (elect_one): one token, 2 of 64 experts,
+// H = 4096, I = 2048: 34.4 us against 39.5 behind a test of the lane.  Where
+// memory is the bound throughout it costs 1 to 2% (the last case below).
 // Precision: the MMA's operands are bf16, but a hidden value, and an e4m3 code
 // times its scale, are not bf16 values.  Both are split into a bf16 value and
 // the bf16 value of the rest (16 bits together), which stand side by side as
 // columns of one B tile; the epilogue adds the two columns.  An MMA this narrow
-// takes as long as its A tile (58 cycles measured, a third of the time that the
-// tile takes to arrive), so the second part costs next to nothing.
+// takes as long as the read of its A tile (37 cycles measured, a fifth of the
+// time that the tile takes to arrive), so the second part costs next to nothing.
 // The blocks meet twice (a cooperative launch, so that all of them are
 // resident): before the hidden rows are read, and before the down products of a
 // token's choices are added up.  The weights do not depend on the hidden rows,
@@ -33,13 +36,13 @@
 // Every block works the routing out for itself (top-k, softmax, each expert's
 // tokens) in shared memory: a launch of its own would take longer.
 // Measured (one call after another in a CUDA graph, other weights each time): one
-// token, 6 of 64 experts, H = 2048, I = 1408: 34.6 us, of which 11 + 5 stream the
+// token, 6 of 64 experts, H = 2048, I = 1408: 32.5 us, of which 10 + 4 stream the
 // weights; the rest is latency (routing 4 us, the two meetings, the last sum).
-// 16 tokens of these: 132 us, 6.2 TB/s; 64 tokens over 256 experts, H = 7168,
-// I = 2048: 2.83 ms, 6.9 TB/s (a copy on the same GPU: 6.7).  Three launches, with
-// the down projections' overlapping the up projections' (35, 139 us and 2.82 ms),
-// did as well for one token and worse in between: each launch worked the routing
-// out anew.  Dot products by warps, without tensor cores: 82 us, 439 us, 12.2 ms.
+// 16 tokens of these: 130 us, 6.2 TB/s; 64 tokens over 256 experts, H = 7168,
+// I = 2048: 2.88 ms, 6.8 TB/s (a copy on the same GPU: 6.7).  Three launches, with
+// the down projections' overlapping the up projections', were as fast for one token
+// and slower in between (139 us for the 16 tokens, where one launch had 132): each
+// launch worked the routing out anew.  Dot products by warps, without tensor cores: 82 us, 439 us, 12.2 ms.
 // Every wait is bounded; one that gives up records MOE_ERR_TIMEOUT in the
 // workspace status word.
 #include <atomic>
