@@ -399,6 +399,7 @@ __device__ __forceinline__ bool wait_for_blocks(const LayerArgs& a, int which, u
         here = __all_sync(0xFFFFFFFFu, here);
     }
     asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    __syncwarp();                                          // what one lane has seen, all have
     return here;
 }
 
@@ -692,8 +693,10 @@ __device__ __forceinline__ void load_tokens(const LayerArgs& a, const Routing& r
                 if (bar_wait(bar, parity)) load_stage(a, r, w, m, k, cols, member, tile);
                 else *failed = 1;
             }
-            // each thread orders its writes before the tensor core's reads
+            // each thread orders its writes before the tensor core's reads, and the warp
+            // its threads' before the one arrival
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
             if (__any_sync(0xFFFFFFFFu, *failed != 0)) return;
             if (lane == 0) mbar_arrive(smem_addr(&full[s]));
         }
