@@ -403,3 +403,73 @@ def test_refusals():
         call(x=q)                                          # codes without scales
     with pytest.raises(ValueError):
         call(x=q, x_scales=torch.ones((3, 4), device="cuda"))
+
+
+def _fill(byte, first, last):
+    return lambda ws: ws[first:last].fill_(byte)
+
+
+def _small_backward(ws):
+    moe.moe_rmsnorm_backward(torch.ones((1, 128), device="cuda"), torch.ones((1, 128), device="cuda"),
+                             torch.ones(128, device="cuda"), workspace=ws)
+
+
+def _router(ws):
+    moe.moe_route(torch.eye(16, device="cuda"), 2, workspace=ws)
+
+
+def _chunks(ws):
+    moe.moe_sort_chunks(torch.ones((8, 3), device="cuda"),
+                        torch.full((4,), 2, dtype=torch.int32, device="cuda"),
+                        torch.arange(4, dtype=torch.int32, device="cuda"), workspace=ws)
+
+
+WRITERS = {"nobody": lambda ws: None, "head": _fill(0, 0, 512), "epoch": _fill(0x5A, 256, 264),
+           "second flags": _fill(0, 512 + 160 * 8, 512 + 320 * 8), "everything": _fill(0xFF, 0, None),
+           "backward": _small_backward, "router": _router, "chunks": _chunks}
+
+
+@pytest.mark.parametrize("writer", WRITERS)
+@pytest.mark.parametrize("T,E,k,H,I", [(16, 32, 4, 512, 256), (1, 8, 2, 256, 128), (9, 64, 6, 2048, 1408)])
+def test_replays_between_which_others_write_the_workspace(writer, T, E, k, H, I):
+    """A captured layer repeats its call; what another node of the graph leaves in the
+    workspace is the same after every replay.  Every replay has other tokens and other
+    choices, and the bits of a call by itself."""
+    layer = Layer(E, H, I, 31)
+    rng = np.random.default_rng(32)
+    sets = []
+    for _ in range(6):
+        x = to_dev(wl.f32_to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32)))
+        lg = to_dev(rng.standard_normal((T, E)).astype(np.float32))
+        sets.append((x, lg, moe.moe_layer_decode(x, lg, k, layer.up_p, layer.down_p)[0]))
+    n = max(moe.moe_layer_decode_workspace_size(T, E, k, H, I), moe.moe_rmsnorm_backward_workspace_size(1, 128),
+            moe.moe_route_workspace_size(16, 16, 2), moe.moe_sort_chunks_workspace_size(4))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    x, lg = sets[0][0].clone(), sets[0][1].clone()
+    WRITERS[writer](ws)                                   # (their first call outside the capture)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = moe.moe_layer_decode(x, lg, k, layer.up_p, layer.down_p, workspace=ws)[0]
+        status = ws[:4].clone()
+        WRITERS[writer](ws)
+    for xs, ls, ref in sets + sets[::-1]:
+        x.copy_(xs)
+        lg.copy_(ls)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (status == 0).all()
+        assert torch.equal(out, ref)
+
+
+def test_a_call_leaves_no_flag_of_its_first_meeting():
+    """Where a later call with the same token would take it: bytes 512 to 1791.  The
+    second meeting's, behind them, are cleared by the blocks that set them."""
+    layer = Layer(8, 256, 128, 33)
+    x = to_dev(wl.f32_to_bf16_bits(np.random.default_rng(34).standard_normal((3, 256)).astype(np.float32)))
+    ws = torch.full((moe.moe_layer_decode_workspace_size(3, 8, 2, 256, 128),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    moe.moe_layer_decode(x, torch.zeros((3, 8), device="cuda"), 2, layer.up_p, layer.down_p, workspace=ws)
+    assert (ws[512:512 + 160 * 8] == 0).all()
+    assert moe.moe_workspace_status(ws) == 0

@@ -71,7 +71,7 @@ constexpr int kMaxBlocks = 160;
 
 // What the blocks meet by, at the same place of every workspace.
 struct Meeting {
-    uint64_t epoch;                       // whatever the last call left
+    uint64_t epoch;                       // the token of the last call, if nobody wrote over it
     uint64_t pad[31];
     uint64_t flag[2][kMaxBlocks];         // a block sets its own to the call's token
 };
@@ -360,12 +360,19 @@ __device__ __forceinline__ void route(const LayerArgs& a, const Routing& r, bool
 
 // ----------------------------------------------------------------- meeting
 
-// The token that the blocks of this call meet by: the epoch that the last call
-// left in the workspace and the call's own nonce, mixed (the finalizer of
-// Steele, Lea & Flood, "Fast splittable pseudorandom number generators", 2014).
-// The epoch changes with every call, so a replayed graph, whose nonce does not,
-// meets by other tokens than before; the workspace may hold anything, because
-// flags that nobody set equal a 64-bit token by chance only.
+// The token that the blocks of this call meet by: the epoch word of the workspace
+// and the call's own nonce, mixed (the finalizer of Steele, Lea & Flood, "Fast
+// splittable pseudorandom number generators", 2014).  Whatever the workspace
+// holds, a flag must not equal the token before its block has set it.  Data of
+// other calls does so by chance only, with 64 bits.  Flags of an earlier call are
+// the danger: a replayed graph repeats its nonce, and where another of its nodes
+// writes the epoch word, the token too.  So no call leaves a flag that a later one
+// could take:
+//   - a block clears its flag of the second meeting before it arrives at the first,
+//     and nobody reads those flags before the first meeting is over;
+//   - block 0 clears the flags of the first meeting after the second, at which a
+//     block arrives only once it has read them for the last time, or without reading
+//     them if it has nothing to wait for.
 __device__ __forceinline__ uint64_t meeting_token(uint64_t epoch, uint64_t nonce) {
     uint64_t z = epoch + nonce * 0x9E3779B97F4A7C15ull;
     z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
@@ -551,6 +558,13 @@ __device__ __forceinline__ bool any_epilogue(bool v) {
     return r != 0;
 }
 
+// Threads that share 4 columns of the last sum: 8 while that leaves each at most one such
+// share; threads of all shares (a multiple of a warp's).
+__device__ __forceinline__ int sum_lanes(const LayerArgs& a) {
+    return a.T * (a.H / 4) * 8 <= int(gridDim.x) * kThreads ? 8 : 1;
+}
+__device__ __forceinline__ int sum_threads(const LayerArgs& a) { return a.T * (a.H / 4) * sum_lanes(a); }
+
 // out[t] = sum over the choices of the weighted down products.  `lanes`
 // neighbouring threads have 4 columns of a token, each a share of the choices
 // (and of their parts); the order of the sum depends on `lanes` alone.
@@ -712,6 +726,7 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
     // a phase has its own barriers of the ring, and a ring of its own shape
     __shared__ __align__(8) uint64_t full_a[2][kMaxStages], full_b[2][kMaxStages], empty[2][kMaxStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t up_done, met;         // once each
     __shared__ uint32_t s_tmem;
     __shared__ uint64_t s_token;
     __shared__ volatile int s_failed;
@@ -736,6 +751,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         if (s < 2) {
             mbar_init(smem_addr(p ? &acc_full[s] : &acc_empty[s]), p ? 1 : 128);
         } else if (threadIdx.x == 2) {
+            mbar_init(smem_addr(&up_done), 1);
+            mbar_init(smem_addr(&met), 1);
             s_failed = 0;
         }
         mbar_fence_init();
@@ -756,6 +773,8 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         uint64_t epoch;
         asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(epoch) : "l"(&a.meeting->epoch) : "memory");
         s_token = meeting_token(epoch, a.nonce);
+        asm volatile("st.relaxed.gpu.global.u64 [%0], %1;"
+                     :: "l"(&a.meeting->flag[1][blockIdx.x]), "l"(uint64_t(0)) : "memory");
     }
     tc_fence_before();
     route(a, r, a.logits && blockIdx.x == 0);
@@ -877,8 +896,15 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         }
     } else if (warp == kEpilogue - 1) {
         // ------------------------------ waits for the other blocks; B tiles, down phase
-        if (!wait_for_blocks(a, 0, s_token)) s_failed = 1;
+        // (and for its own block's MMAs, which have to have read the ring that the copies go to)
+        // A block with neither down products nor a share of the last sum waits for nobody.
+        if (int(blockIdx.x) < s_work[1].items || int(blockIdx.x) * kThreads < sum_threads(a)) {
+            if (!wait_for_blocks(a, 0, s_token)) s_failed = 1;
+            if (!bar_wait(smem_addr(&up_done), 0)) s_failed = 1;
+            __syncwarp();
+        }
         if (elect_one()) {
+            mbar_arrive(smem_addr(&met));
             // the hidden rows, which other blocks' threads wrote and copies now read
             asm volatile("fence.proxy.async;" ::: "memory");
             const Work w = s_work[1];
@@ -993,7 +1019,11 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
             }
             // (also where this block gave up: the others go on, and end)
             bar_epilogue();
-            if (row == 0) arrive(a, phase, s_token);
+            if (row == 0) {
+                if (up) mbar_arrive(smem_addr(&up_done));
+                else if (!bar_wait(smem_addr(&met), 0)) s_failed = 1;
+                arrive(a, phase, s_token);
+            }
         }
     }
     tc_fence_before();
@@ -1003,23 +1033,25 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
                      :: "r"(tmem), "r"(kTmemCols) : "memory");
     // the sum over a token's choices, of every block's products
-    // (8 threads share 4 columns while that leaves each at most one of them; the
-    // number of threads is a multiple of a warp's)
-    const int quads = a.T * (a.H / 4), lanes = quads * 8 <= int(gridDim.x) * kThreads ? 8 : 1;
-    if (int(blockIdx.x) * kThreads < quads * lanes) {
+    const int lanes = sum_lanes(a);
+    if (int(blockIdx.x) * kThreads < sum_threads(a)) {
         if (warp == 0) {
             const bool there = wait_for_blocks(a, 1, s_token);
             if (lane == 0) s_late = !there;
         }
         __syncthreads();
         if (s_late) s_failed = 1;
+        // block 0 (which has a share of the sum, whatever the shape): nobody reads this
+        // call's epoch or the first meeting's flags any more
+        if (blockIdx.x == 0) {
+            if (threadIdx.x < kMaxBlocks) a.meeting->flag[0][threadIdx.x] = 0;
+            if (threadIdx.x == kMaxBlocks) a.meeting->epoch = s_token;
+        }
         const Work w = s_work[1];
 #pragma unroll 1
-        for (int i = blockIdx.x * kThreads + threadIdx.x; i < quads * lanes; i += gridDim.x * kThreads)
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < sum_threads(a); i += gridDim.x * kThreads)
             add_up(a, r, w, lanes, i);
     }
-    // every block has met block 0 once: nobody reads this call's epoch any more
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.meeting->epoch = s_token;
     if (threadIdx.x == 0 && s_failed) {
         a.header->status = MOE_ERR_TIMEOUT;
         a.header->detail = blockIdx.x;
