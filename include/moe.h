@@ -480,7 +480,8 @@ moe_status_t moe_permute_quantize_fp8(const void* x, int64_t T, int64_t H, int b
  *   h = round(x + residual)             stored in residual_out; h = x if
  *                                       residual is NULL (residual_out unused)
  *   out = h * r * weight,  r = 1 / sqrt(mean over the row of h^2 + eps)
- * in float32, each output rounded once; the norm is that of h as stored.
+ * in float32, each output rounded once; the norm is that of h as stored.  A row's
+ * sum of squares has to stay within float32's range.
  *   x, residual, residual_out, out [T,H] (dtype: MOE_F32 or MOE_BF16);
  *   weight [H] (weight_dtype: MOE_F32 or MOE_BF16); eps >= 0.
  * residual_out and out may each be x or residual itself (the stream updated in
@@ -507,7 +508,8 @@ moe_status_t moe_rmsnorm_quantize_fp8(const void* x, const void* residual, moe_d
 
 /* moe_rmsnorm_backward: with grad_y the gradient of out, and grad_h (NULL:
  * none) the gradient that reaches h past the norm, on the residual stream:
- *   grad_x = r (grad_y w) - h r^3 mean(grad_y w h) + grad_h   (rounded once)
+ *   grad_x = r (grad_y w) - h r^3 mean(grad_y w h) + grad_h   (rounded once; r^3
+ *            itself is not formed and need not be a float32)
  *   grad_weight = sum over the rows of grad_y h r             (float32)
  * grad_x is the gradient of x and of residual alike.  h is what moe_rmsnorm
  * stored (residual_out, or x without a residual).

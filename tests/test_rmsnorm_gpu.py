@@ -429,3 +429,38 @@ def test_refusals():
         moe.moe_rmsnorm_backward(x, x[:2], w)
     with pytest.raises(ValueError):
         moe.moe_rmsnorm_backward(x, x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------ rows far from one in size
+
+@pytest.mark.parametrize("T,H,off", [(6, 256, 0), (400, 2048, 0), (5, 77, 0), (3, 1001, 0), (4, 520, 1),
+                                     (2, 20000, 0), (2, 33001, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rms,eps", [(1e15, EPS), (1e-14, 0.0)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_backward_of_large_and_small_rows(T, H, off, dtype, rms, eps, residual):
+    """Rows of 1e15 and 1e-14: their norm and its gradient are ordinary numbers, though
+    r^3 is none in float32.  grad_y leans on h, so that the term of the mean counts.  off:
+    rows that start so many elements off a 16-byte boundary.  The error is that of the
+    backward's other tests: r three times, the mean's D additions, and products."""
+    rng = np.random.default_rng(T + H)
+    unit = rng.standard_normal((T, H)).astype(np.float32)
+    h = wl.as_activation((unit * rms).astype(np.float32), dtype)
+    g = wl.as_activation((unit + 0.3 * rng.standard_normal((T, H))).astype(np.float32), dtype)
+    gh = wl.as_activation((rng.standard_normal((T, H)) / rms).astype(np.float32), dtype) if residual else None
+    w = wl.as_activation((1.0 + 0.1 * rng.standard_normal(H)).astype(np.float32), dtype)
+
+    def put(a):
+        t = to_dev(a)
+        flat = torch.zeros(t.numel() + off, dtype=t.dtype, device="cuda")
+        flat[off:] = t.view(-1)
+        return flat[off:].view(t.shape)
+    gx, gw = moe.moe_rmsnorm_backward(put(g), put(h), to_dev(w), eps=eps,
+                                      grad_h=None if gh is None else put(gh))
+    gx64, size, gw64, gw_size = _backward64(g, h, w, gh, eps)
+    D = _depth(H)
+    assert (np.abs(_val(gx) - gx64) <= (2.5 * D + 24) * U * size + HALF[dtype] * np.abs(gx64)).all()
+    assert (np.abs(_val(gw) - gw64) <= (D / 2 + 10 + T) * U * gw_size).all()
+    y, _ = moe.moe_rmsnorm(put(h), to_dev(w), eps=eps)
+    y64, _ = _norm64(h, w, eps)
+    assert (np.abs(_val(y) - y64) <= ((D / 2 + 8) * U + HALF[dtype]) * np.abs(y64)).all()

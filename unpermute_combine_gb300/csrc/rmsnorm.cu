@@ -15,6 +15,9 @@
 //   grad_x = r (g w) - h r^3 mean(g w h) + gh
 //   grad_weight = sum over the rows of g h r      (float32, fixed order)
 // r is recomputed: h has to be read anyway, and both sums share one reduction.
+// With the normed row n = h r the first is r (g w - n (r mean(g w h))) + gh, and so
+// it is computed: r^3 leaves float32's range where rows are as large as 1e13 or as
+// small as 1e-13.
 #include "pipeline.cuh"
 
 namespace moe {
@@ -574,7 +577,7 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
             break;
         }
         const float r = rsqrtf(ss / float(a.H) + a.eps);
-        const float b = r * r * r * (dot / float(a.H));
+        const float b = r * (dot / float(a.H));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
@@ -585,8 +588,9 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
                 values(weight[v], w);
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
-                    dw[v][i] = fmaf(gv[i], hv[i] * r, dw[v][i]);
-                    o[i] = r * (gv[i] * w[i]) - hv[i] * b;
+                    const float n = hv[i] * r;
+                    dw[v][i] = fmaf(gv[i], n, dw[v][i]);
+                    o[i] = r * fmaf(-n, b, gv[i] * w[i]);
                 }
                 if (a.gh) {
                     float e[kChunk];
@@ -667,14 +671,15 @@ rmsnorm_backward_odd_kernel(const BwdArgs a) {
         }
         const float2 t = block_sum2(ss, dot, s_part[turn]);
         const float r = rsqrtf(t.x / float(a.H) + a.eps);
-        const float b = r * r * r * (t.y / float(a.H));
+        const float b = r * (t.y / float(a.H));
 #pragma unroll
         for (int v = 0; v < kChunk; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
-            dw[v] = fmaf(g[v], h[v] * r, dw[v]);
+            const float n = h[v] * r;
+            dw[v] = fmaf(g[v], n, dw[v]);
             if (c < H)
                 store1(static_cast<X*>(a.gx) + row * a.H + c,
-                       r * (g[v] * load1(static_cast<const W*>(a.weight) + c)) - h[v] * b + e[v]);
+                       fmaf(r, fmaf(-n, b, g[v] * load1(static_cast<const W*>(a.weight) + c)), e[v]));
             h[v] = hn[v];
             g[v] = gn[v];
         }
@@ -707,11 +712,11 @@ rmsnorm_backward_long_kernel(const BwdArgs a) {
         }
         const float2 t = block_sum2(ss, dot, s_part[turn]);
         const float r = rsqrtf(t.x / float(a.H) + a.eps);
-        const float b = r * r * r * (t.y / float(a.H));
+        const float b = r * (t.y / float(a.H));
         for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
-            const float hv = load1(h + i), gv = load1(g + i);
-            part[i] = fmaf(gv, hv * r, part[i]);
-            float o = r * (gv * load1(static_cast<const W*>(a.weight) + i)) - hv * b;
+            const float n = load1(h + i) * r, gv = load1(g + i);
+            part[i] = fmaf(gv, n, part[i]);
+            float o = r * fmaf(-n, b, gv * load1(static_cast<const W*>(a.weight) + i));
             if (a.gh) o += load1(static_cast<const X*>(a.gh) + row * a.H + i);
             store1(static_cast<X*>(a.gx) + row * a.H + i, o);
         }
