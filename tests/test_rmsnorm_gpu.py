@@ -464,3 +464,66 @@ def test_backward_of_large_and_small_rows(T, H, off, dtype, rms, eps, residual):
     y, _ = moe.moe_rmsnorm(put(h), to_dev(w), eps=eps)
     y64, _ = _norm64(h, w, eps)
     assert (np.abs(_val(y) - y64) <= ((D / 2 + 8) * U + HALF[dtype]) * np.abs(y64)).all()
+
+
+@pytest.mark.parametrize("T,H,block", [(2048, 4096, 128), (3, 512, 32), (40, 8192, 256), (700, 1024, 64)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_codes_are_those_of_the_quotient(T, H, block, residual):
+    """scale = amax / 448 and code = e4m3(y / scale), each quotient rounded as float32's
+    division rounds it, bit for bit, from the float32 y that moe_rmsnorm gives (a row's
+    sum has the same order in both).  Blocks of scales below 2^-90 and above 2^60, of
+    zeros of both signs and of an infinite y among them."""
+    rng = np.random.default_rng(T + H)
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    res = rng.standard_normal((T, H)).astype(np.float32) if residual else None
+    w = (1.0 + 0.1 * rng.standard_normal(H)).astype(np.float32)
+    w[:block] *= np.float32(2.0 ** -87)
+    w[block:2 * block] *= np.float32(2.0 ** -100)
+    w[2 * block:3 * block] *= np.float32(2.0 ** 70)
+    w[3 * block:4 * block:2] = 0.0                       # y = 0 or -0 beside others
+    w[4 * block:5 * block] = 0.0
+    if H // block > 6:
+        w[5 * block + 3] = np.inf
+    xd, rd, wd = to_dev(x), None if res is None else to_dev(res), to_dev(w)
+    y, _ = moe.moe_rmsnorm(xd, wd, residual=rd)
+    q, sc, _ = moe.moe_rmsnorm_quantize_fp8(xd, wd, residual=rd, block=block)
+    y = y.cpu().view(T, H // block, block)
+    amax = y.abs().amax(2)
+    s = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+    assert torch.equal(sc.cpu(), s)
+    quot = y / s[:, :, None]
+    want = quot.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(T, H)
+    got, want = q.cpu().view(torch.uint8), want.view(torch.uint8)
+    nan = torch.isnan(quot).view(T, H)
+    assert ((got & 0x7F) == 0x7F)[nan].all()
+    assert torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("block", [32, 256])
+def test_codes_next_to_a_boundary(dtype, block):
+    """Rows of ones with eps = 0 have y = weight, so that a block's scale and quotients can
+    be chosen: every scale has values one or two float steps around midpoints of
+    neighbouring e4m3 values, where the last bit of the quotient decides."""
+    T, H = 2, 32768
+    rng = np.random.default_rng(block)
+    mids = np.concatenate([(1 + (2 * np.arange(8) + 1) / 16)[None, :] * 2.0 ** np.arange(-6, 9)[:, None],
+                           ((np.arange(8) + 0.5) * 2.0 ** -9)[None, :]]).ravel()
+    mids = mids[mids < 448]
+    for turn in range(8):
+        n = H // block
+        s = (1.0 + rng.integers(0, 1 << 23, n) * 2.0 ** -23).astype(np.float32)
+        s[:4] = np.float32(2.0) - np.float32(2.0 ** -23) * np.arange(1, 5, dtype=np.float32)
+        s *= (2.0 ** rng.integers(-95, 100, n)).astype(np.float32)
+        amax = s * np.float32(448)
+        s = amax / np.float32(448)                        # the scale that the kernel finds
+        w = (rng.choice(mids, (n, block)) * s.astype(np.float64)[:, None]).astype(np.float32)
+        w = (w.view(np.int32) + rng.integers(-2, 3, w.shape).astype(np.int32)).view(np.float32)
+        w *= rng.choice(np.array([-1, 1], np.float32), w.shape)
+        w[:, turn] = amax
+        ones = to_dev(wl.as_activation(np.ones((T, H), np.float32), dtype))
+        q, sc, _ = moe.moe_rmsnorm_quantize_fp8(ones, to_dev(w.ravel()), eps=0.0, block=block)
+        assert (to_host(sc) == s[None, :]).all()
+        want = torch.from_numpy(w / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        got = q.cpu().view(torch.uint8)
+        assert (got == want.view(torch.uint8).view(1, H)).all()

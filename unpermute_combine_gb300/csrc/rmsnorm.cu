@@ -177,15 +177,54 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// four floats -> four e4m3 bytes of f / s, with inv = 1 / s: a product costs a tenth
-// of a division, and is off by two float ulp, where y is by several.
-__device__ __forceinline__ uint32_t q4(const float* f, float inv) {
-    return e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
+// Products of two floats at once.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-// The same by division, for a scale whose reciprocal overflows.
-__device__ __forceinline__ uint32_t q4_divided(const float* f, float s) {
-    return e4m3x2(__fdiv_rn(f[0], s), __fdiv_rn(f[1], s)) |
-           (e4m3x2(__fdiv_rn(f[2], s), __fdiv_rn(f[3], s)) << 16);
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Two e4m3 bytes of y / s, each the code of the correctly rounded quotient: the product
+// with inv = 1 / s and its remainder put back (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  Of -y and -inv, so that the
+// zeros keep their signs.
+__device__ __forceinline__ uint32_t quotients(float ny0, float ny1, uint64_t s, uint64_t ninv) {
+    const uint64_t ny = both(ny0, ny1), q = mul2(ny, ninv), r = fma2(fma2(q, s, ny), ninv, q);
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+    return e4m3x2(a, b);
+}
+// 8 negated floats -> 8 e4m3 bytes of y / s.  The reciprocal is an approximation (an ulp
+// off) and a Newton step: the rounded 1 / s, or for a few s an ulp off.  Every s with
+// every y next to a boundary of two codes was compared with the division, from
+// approximations up to 3 ulp off: the codes are the same, but for one y of the s whose
+// significand is all ones.  That s is divided by, as are an infinite one and those so
+// small that a remainder underflows (a code other than 0 has a quotient of 2^-10 or more,
+// whose remainder is a multiple of 2^-56 s).  8192 rows of 4096: 46.5 us, 46.1 with the
+// product alone (which had other codes now and then), 55.0 with divisions throughout.
+__device__ __forceinline__ uint2 q8(const float* ny, float s) {
+    if (s >= 0x1p-90f && s <= 0x1.fffffep+127f && (~__float_as_uint(s) & 0x7FFFFFu)) {
+        float ninv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ninv) : "f"(-s));
+        ninv = fmaf(fmaf(s, ninv, 1.0f), ninv, ninv);
+        const uint64_t ss = both(s, s), ii = both(ninv, ninv);
+        return make_uint2(quotients(ny[0], ny[1], ss, ii) | quotients(ny[2], ny[3], ss, ii) << 16,
+                          quotients(ny[4], ny[5], ss, ii) | quotients(ny[6], ny[7], ss, ii) << 16);
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = e4m3x2(__fdiv_rn(ny[2 * i], -s), __fdiv_rn(ny[2 * i + 1], -s));
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
 // Sum over a row's threads (blockDim.x of them: a warp, or the block), the same
@@ -222,7 +261,7 @@ struct NormArgs {
 // A row to blockDim.x threads (a warp, blockDim.y rows a block; or the block), V
 // chunks a thread held in registers between the two passes over the row.  Bound
 // by memory: 16384 rows of 7168 in bf16 with a residual take 136 us, 6.9 TB/s (a
-// copy: 6.7); with e4m3 output 153 us, 5.3 TB/s, where the instructions of the
+// copy: 6.7); with e4m3 output 156 us, 5.3 TB/s, where the instructions of the
 // quantization fill 60% of the issue slots; rows of 7001 elements 150 us.  64
 // registers where a thread has 64 bytes: with 76, the e4m3 form took 176 us.
 template <typename X, typename W, int V, bool kQuant, bool kShift>
@@ -278,7 +317,8 @@ rmsnorm_kernel(const NormArgs a) {
                 for (int i = 0; i < kChunk; ++i) ss = fmaf(f[i], f[i], ss);
             }
         }
-        const float r = rsqrtf(block_sum(ss, s_part[turn]) / float(a.H) + a.eps);
+        const float root = rsqrtf(block_sum(ss, s_part[turn]) / float(a.H) + a.eps);
+        const float r = kQuant ? -root : root;             // (q8 takes -y)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = threadIdx.x + v * blockDim.x;
@@ -309,9 +349,7 @@ rmsnorm_kernel(const NormArgs a) {
                 if (!(s >= 0x1p-126f)) s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
                 if (c < chunks) {
                     uint2* q = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.H);
-                    const float inv = __fdividef(1.0f, s);
-                    q[c] = s >= 0x1p-126f ? make_uint2(q4(y, inv), q4(y + 4, inv))
-                                          : make_uint2(q4_divided(y, s), q4_divided(y + 4, s));
+                    q[c] = q8(y, s);
                     if (c % a.lanes == 0) a.scales[row * (chunks / a.lanes) + c / a.lanes] = s;
                 }
             }
