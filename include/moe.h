@@ -514,8 +514,8 @@ moe_status_t moe_rmsnorm_quantize_fp8(const void* x, const void* residual, moe_d
  * grad_x is the gradient of x and of residual alike.  h is what moe_rmsnorm
  * stored (residual_out, or x without a residual).
  *   grad_y, grad_h, h, grad_x [T,H] (dtype); grad_weight [H] float, written
- *   completely (zeros for T = 0), in an order that only T, H and the
- *   alignment decide.
+ *   completely (zeros for T = 0), summed in an order that only T, H, dtype, the
+ *   alignment of the tensors and the GPU's number of SMs decide.
  * grad_x may be grad_y, grad_h or h itself; no other overlap.  Workspace:
  * moe_rmsnorm_backward_workspace_size(T, H) bytes, which may hold anything.
  * Rows in memory that starts on 16-byte boundaries come by bulk copies; a

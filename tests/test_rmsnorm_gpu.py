@@ -527,3 +527,48 @@ def test_codes_next_to_a_boundary(dtype, block):
         want = torch.from_numpy(w / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
         got = q.cpu().view(torch.uint8)
         assert (got == want.view(torch.uint8).view(1, H)).all()
+
+
+@pytest.mark.parametrize("T,H", [(4000, 2048), (700, 1001), (900, 4096), (400, 8528), (300, 8544),
+                                 (310, 9001), (200, 12792), (160, 12800), (40, 20000), (3, 8), (2500, 24)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_grad_weight_does_not_depend_on_grad_h(T, H, dtype):
+    """grad_h is not in grad_weight's formula, and changes no bit of it; wide float32
+    rows, of which a ring has only two tensors', among them."""
+    rng = np.random.default_rng(T + H)
+    g, h, gh = (_act(rng, (T, H), dtype) for _ in range(3))
+    w = wl.as_activation((1.0 + 0.1 * rng.standard_normal(H)).astype(np.float32), dtype)
+    gd, hd, ghd, wd = to_dev(g), to_dev(h), to_dev(gh), to_dev(w)
+    gx0, gw0 = moe.moe_rmsnorm_backward(gd, hd, wd)
+    gx1, gw1 = moe.moe_rmsnorm_backward(gd, hd, wd, grad_h=ghd)
+    assert torch.equal(gw0, gw1)
+    for k, extra in ((0, None), (1, gh)):
+        gx64, size, gw64, gw_size = _backward64(g, h, w, extra, EPS)
+        D = _depth(H)
+        got = (gx0, gx1)[k]
+        assert (np.abs(_val(got) - gx64) <= (2.5 * D + 24) * U * size + HALF[dtype] * np.abs(gx64)).all()
+    assert (np.abs(_val(gw0) - gw64) <= (D / 2 + 10 + T) * U * gw_size).all()
+    for k in range(3):                                     # in place
+        t = [gd.clone(), hd.clone(), ghd.clone()]
+        gx, gw = moe.moe_rmsnorm_backward(t[0], t[1], wd, grad_h=t[2], grad_x=t[k])
+        assert torch.equal(gx, gx1) and torch.equal(gw, gw1)
+
+
+@pytest.mark.parametrize("T,H", [(5, 8600), (3, 12790), (2, 12792), (1, 9001)])
+def test_wide_float32_rows_between_others(T, H):
+    """What lies before and behind wide rows and their grad_h, NaN here, is neither used
+    nor changed."""
+    rng = np.random.default_rng(H)
+    a = [_act(rng, (T, H), "f32") for _ in range(3)]
+    w = (1.0 + 0.1 * rng.standard_normal(H)).astype(np.float32)
+    big = [torch.full((64 + T * H + 64,), float("nan"), device="cuda") for _ in range(4)]
+    rows = [b[64:64 + T * H].view(T, H) for b in big]
+    for r, v in zip(rows, a):
+        r.copy_(to_dev(v))
+    gx, gw = moe.moe_rmsnorm_backward(rows[0], rows[1], to_dev(w), grad_h=rows[2], grad_x=rows[3])
+    gx64, size, gw64, gw_size = _backward64(a[0], a[1], w, a[2], EPS)
+    D = _depth(H)
+    assert (np.abs(_val(gx) - gx64) <= (2.5 * D + 24) * U * size + U * np.abs(gx64)).all()
+    assert (np.abs(_val(gw) - gw64) <= (D / 2 + 10 + T) * U * gw_size).all()
+    for b in big:
+        assert torch.isnan(b[:64]).all() and torch.isnan(b[64 + T * H:]).all()

@@ -443,6 +443,7 @@ struct BwdArgs {
     int64_t H;
     float eps;
     int ring;                 // rows that a team has in shared memory
+    bool ring_gh;             // rows of gh among them
 };
 
 // Sums of two values over the block at once.
@@ -473,9 +474,9 @@ __host__ __device__ constexpr uint32_t slot_size(int64_t H, bool three) {
 }
 
 // Rows in teams of blockDim.x threads, blockDim.y teams a block.  A team has a ring
-// of rows in shared memory (h, grad_y and grad_h of each), which bulk copies fill
-// rows ahead, so that reading goes on while a row waits for its sums; V chunks a
-// thread.  The columns' shares of grad_weight stay in registers over all rows of
+// of rows in shared memory (h, grad_y and grad_h of each, or the first two where only
+// they have room twice), which bulk copies fill rows ahead, so that reading goes on
+// while a row waits for its sums; V chunks a thread.  The columns' shares of grad_weight stay in registers over all rows of
 // the block; its teams' shares are added up at the end, in order, and the blocks'
 // by rmsnorm_grad_weight_kernel.
 // Bound by memory on long batches (16384 rows of 7168 in bf16 with grad_h: 145 us,
@@ -498,8 +499,8 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
     // team's rows, and a thread's chunks are the same columns in all of them)
     const int shift = kShift ? row_shift<X>(first, a.H) : 0;
     const int chunks = (H + shift + kChunk - 1) / kChunk;
-    const uint32_t slot_bytes = slot_size<X, kShift>(a.H, a.gh != nullptr);
-    const uint32_t row_bytes = slot_bytes / (a.gh ? 3 : 2);
+    const uint32_t slot_bytes = slot_size<X, kShift>(a.H, a.ring_gh);
+    const uint32_t row_bytes = slot_bytes / (a.ring_gh ? 3 : 2);
     uint8_t* ring = smem + size_t(team) * a.ring * slot_bytes;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.ring; ++i) mbar_init(smem_addr(&full[team][i]), 1);
@@ -522,11 +523,11 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
         const uint32_t bar = smem_addr(&full[team][slot]), dst = smem_addr(ring + slot * slot_bytes);
         const uint32_t bytes = uint32_t(brought(n)) * uint32_t(sizeof(X));
         const int64_t at = (first + n * step) * a.H - shift;
-        mbar_expect_tx(bar, bytes * (a.gh ? 3 : 2));
+        mbar_expect_tx(bar, bytes * (a.ring_gh ? 3 : 2));
         if (kShift && bytes == 0) return;
         bulk_load(dst, static_cast<const X*>(a.h) + at, bytes, bar);
         bulk_load(dst + row_bytes, static_cast<const X*>(a.g) + at, bytes, bar);
-        if (a.gh) bulk_load(dst + 2 * row_bytes, static_cast<const X*>(a.gh) + at, bytes, bar);
+        if (a.ring_gh) bulk_load(dst + 2 * row_bytes, static_cast<const X*>(a.gh) + at, bytes, bar);
     };
     if (threadIdx.x == 0)
         for (int64_t n = 0; n < rows && n < a.ring; ++n) fill(n);
@@ -559,7 +560,7 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
                     const int pitch = int(row_bytes / sizeof(X));
                     edge[0] = inside ? static_cast<const X*>(a.h)[at] : X(0);
                     edge[pitch] = inside ? static_cast<const X*>(a.g)[at] : X(0);
-                    if (a.gh) edge[2 * pitch] = inside ? static_cast<const X*>(a.gh)[at] : X(0);
+                    if (a.ring_gh) edge[2 * pitch] = inside ? static_cast<const X*>(a.gh)[at] : X(0);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy
                 }
             }
@@ -630,13 +631,18 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
                     dw[v][i] = fmaf(gv[i], n, dw[v][i]);
                     o[i] = r * fmaf(-n, b, gv[i] * w[i]);
                 }
+                const int64_t at = first + n * step;
                 if (a.gh) {
                     float e[kChunk];
-                    chunk(2, c, e);
+                    if (sizeof(X) == 2 || a.ring_gh)       // (bf16 rows always have room)
+                        chunk(2, c, e);
+                    else
+                        values(load_at<kShift>(static_cast<const X*>(a.gh) + at * a.H, c * kChunk - shift,
+                                               H, (a.T - at) * a.H), e);
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) o[i] += e[i];
                 }
-                X* gx = static_cast<X*>(a.gx) + (first + n * step) * a.H;
+                X* gx = static_cast<X*>(a.gx) + at * a.H;
                 store_at<kShift>(gx, c * kChunk - shift, H, rounded(gx, o));
             }
         }
@@ -866,13 +872,17 @@ moe_status_t dispatch_norm(const NormArgs& a, int dtype, int wdtype, Rows how,
 
 template <typename X, typename W, bool kShift>
 moe_status_t launch_ring(BwdArgs a, unsigned* blocks, cudaStream_t s) {
-    const int64_t slot = slot_size<X, kShift>(a.H, a.gh != nullptr);
-    const int64_t chunks = slot / (a.gh ? 3 : 2) / int64_t(kChunk * sizeof(X));
+    // The teams follow from the size of three tensors' rows, with grad_h or without: the
+    // order of grad_weight's sums is the same.
+    const int64_t most_slot = slot_size<X, kShift>(a.H, true);
+    a.ring_gh = a.gh && 2 * most_slot <= kRingBytes;
+    const int64_t slot = slot_size<X, kShift>(a.H, a.ring_gh);
+    const int64_t chunks = most_slot / 3 / int64_t(kChunk * sizeof(X));
     const int V = chunks > 32 ? 2 : 1;
     const int threads = warps_up((chunks + V - 1) / V);
     // as many teams as fit (16384 rows of 2048 in bf16: 57 us with 8, 98 with 2, 173
     // with 1), but no fewer blocks than SMs for them
-    int teams = int(min64(min64(kMaxThreads / threads, kMaxTeams), kRingBytes / (2 * slot)));
+    int teams = int(min64(min64(kMaxThreads / threads, kMaxTeams), kRingBytes / (2 * most_slot)));
     teams = int(max64(1, min64(teams, (a.T + sm_count() - 1) / sm_count())));
     a.ring = int(min64(kMaxRing, kRingBytes / (teams * slot)));
     int64_t most = min64(sm_count(), kBwdMaxBlocks);
@@ -892,7 +902,7 @@ moe_status_t launch_ring(BwdArgs a, unsigned* blocks, cudaStream_t s) {
 // others as many as help.
 template <typename X, typename W>
 moe_status_t launch_backward(const BwdArgs& a, Rows how, unsigned* blocks, cudaStream_t s) {
-    if (how != kElements && 2 * int64_t(slot_size<X, true>(a.H, a.gh != nullptr)) <= kRingBytes &&
+    if (how != kElements && 2 * int64_t(slot_size<X, true>(a.H, false)) <= kRingBytes &&
         a.H + kChunk <= 2 * kMaxThreads * kChunk) {
         if (how == kVectors) return launch_ring<X, W, false>(a, blocks, s);
         // a shift wants blocks by eights, or no second row for a team
@@ -992,7 +1002,7 @@ extern "C" moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* gra
         workspace_bytes < need)
         return MOE_ERR_WORKSPACE;
     unsigned blocks = 0;
-    const BwdArgs a{grad_y, grad_h, h, weight, grad_x, static_cast<float*>(workspace), T, H, eps, 0};
+    const BwdArgs a{grad_y, grad_h, h, weight, grad_x, static_cast<float*>(workspace), T, H, eps, 0, false};
     const Rows how = rows_of(H, weight, {grad_y, grad_h, h, grad_x});
     moe_status_t r;
     if (dtype == MOE_BF16)
