@@ -473,3 +473,31 @@ def test_a_call_leaves_no_flag_of_its_first_meeting():
     moe.moe_layer_decode(x, torch.zeros((3, 8), device="cuda"), 2, layer.up_p, layer.down_p, workspace=ws)
     assert (ws[512:512 + 160 * 8] == 0).all()
     assert moe.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(6, 8, 2, 256, 128), (40, 4, 2, 512, 256)])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("where", ["up", "gate", "down"])
+def test_infinite_weights(T, E, k, H, I, fp8, where):
+    """An infinite weight makes of the outputs it enters what it makes of them in float64,
+    infinities and NaN at the same places, and touches no other output: rows are kept in
+    two parts, of which a part of 0 or of the other sign must not turn it into NaN."""
+    layer = Layer(E, H, I, 41)
+    if where == "down":
+        layer.down[1, 5, 17], layer.down[2, 70, 200] = 0x7F80, 0xFF80
+    else:                                                 # one row of expert 1's gate or up weights
+        layer.up[1, 9, 33 + (I if where == "up" else 0)] = 0x7F80
+    layer.up_p, layer.down_p = moe.moe_grouped_swiglu_pack(to_dev(layer.up), to_dev(layer.down))
+    rng = np.random.default_rng(42)
+    args, x64 = _x(rng, T, H, fp8)
+    idx, w = wl.random_routing(43, T, E, k)
+    out = moe.moe_layer_decode_indices(topk_idx=to_dev(idx), topk_w=to_dev(w), **args,
+                                       w_up_packed=layer.up_p, w_down_packed=layer.down_p)
+    with np.errstate(all="ignore"):
+        ref, tol = _reference(layer, x64, idx, w, fp8)
+    got = _out64(out)
+    assert not np.isfinite(ref).all()
+    assert (np.isnan(got) == np.isnan(ref)).all()
+    assert (got[np.isinf(ref)] == ref[np.isinf(ref)]).all()
+    fine = np.isfinite(ref)
+    assert (np.abs(got[fine] - ref[fine]) <= tol[fine]).all()

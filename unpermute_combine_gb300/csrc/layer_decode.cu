@@ -971,8 +971,11 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                     if (w.two) {
                         float lo[8];
                         tmem_ld8(acc + b_rows(m.n, true) + c0, lo);
+                        // (an infinite weight times a part that is 0, or of the other sign, would
+                        // make NaN of the infinity that the first part has)
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] += lo[c];
+                        for (int c = 0; c < 8; ++c)
+                            if (fabsf(v[c]) <= 0x1.fffffep+127f) v[c] += lo[c];
                     }
                     if (up) {
                         // The tile's first rows hold the gate, the next ones the up values.  A
