@@ -104,8 +104,6 @@ template <typename X>
 __device__ __forceinline__ void load8(const X* p, float* f) { values(load_raw(p), f); }
 template <typename X>
 __device__ __forceinline__ void shared8(const X* p, float* f) { values(shared_raw(p), f); }
-template <typename X>
-__device__ __forceinline__ void store8(X* p, const float* f) { store_raw(p, rounded(p, f)); }
 // Rows that are no multiple of 16 bytes start off a 16-byte boundary, each by its
 // own shift, but all of a call's tensors by the same one.  Their chunks are those
 // of the aligned memory: chunk c has the elements from 8 c - shift on, and the
