@@ -487,15 +487,17 @@ moe_status_t moe_permute_quantize_fp8(const void* x, int64_t T, int64_t H, int b
  * residual_out and out may each be x or residual itself (the stream updated in
  * place), but not one another (else MOE_ERR_INVALID_ARG); no other overlap.
  * Any H and alignment; tensors that start on 16-byte boundaries take the
- * vectorised paths; one off its elements' boundaries is MOE_ERR_INVALID_ARG.
+ * vectorised paths, others are moved by elements (up to 4 times the time); one
+ * off its elements' boundaries is MOE_ERR_INVALID_ARG.
  *
  * moe_rmsnorm_quantize_fp8: the same norm with the output quantized as
  * moe_quantize_fp8 does, from the float32 values (not from bf16 ones): per
  * block of `block` (32, 64, 128 or 256) elements scale = amax / 448 (1 for an
  * all-zero block) and x_q = e4m3(y / scale), of the rounded float quotient.
  * x_q [T,H] e4m3 bytes, scales [T, H/block] float.  H a multiple of block (else
- * MOE_ERR_INVALID_ARG) and at most 32768 (else MOE_ERR_UNSUPPORTED); x, residual, weight and residual_out
- * 16-byte, x_q 8-byte, scales 4-byte aligned (else MOE_ERR_INVALID_ARG).
+ * MOE_ERR_INVALID_ARG) and at most 32768 (else MOE_ERR_UNSUPPORTED); x, residual,
+ * weight and residual_out 16-byte, x_q 8-byte, scales 4-byte aligned (else
+ * MOE_ERR_INVALID_ARG).
  * residual_out may be x or residual itself. */
 moe_status_t moe_rmsnorm(const void* x, const void* residual, moe_dtype_t dtype,
                          const void* weight, moe_dtype_t weight_dtype, int64_t T, int64_t H,
@@ -535,9 +537,10 @@ moe_status_t moe_rmsnorm_backward(const void* grad_y, const void* grad_h, const 
  * moe_grouped_swiglu ([MOE-OPS] §3, §8, §16; [COMBINE] §1):
  *   out[t] = sum_{j=0..k-1} topk_w[t,j] * y(t, topk_idx[t,j])
  *   y(t,e) = (silu(x_t @ w_gate[e]) * (x_t @ w_up[e])) @ w_down[e]
- * Products are summed in float32, the hidden activation keeps at least 16
- * bits, slots are added in a fixed order and out [T,H] bf16 is rounded once.  The
- * same inputs give the same bits on every call.
+ * Products are summed in float32; the hidden activation, and an e4m3 code times
+ * its scale, keep 16 bits (off by 2^-17 at most); slots are added in a fixed
+ * order and out [T,H] bf16 is rounded once.  The same inputs give the same bits
+ * on every call.
  *
  * moe_layer_decode chooses as moe_route does (the k largest logits, ties to
  * the lower id, softmax over those k) and writes topk_idx [T,k] int32 and

@@ -501,3 +501,33 @@ def test_infinite_weights(T, E, k, H, I, fp8, where):
     assert (got[np.isinf(ref)] == ref[np.isinf(ref)]).all()
     fine = np.isfinite(ref)
     assert (np.abs(got[fine] - ref[fine]) <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("T", [1, 24])
+def test_a_block_with_its_router(T):
+    """The norm's rows go to a router and to the layer, in bf16 and quantized to e4m3; the
+    next norm adds the layer's rows to the stream.  Each step against float64 from what
+    the step before left."""
+    E, k, H, I = 12, 3, 512, 256
+    layer = Layer(E, H, I, 51)
+    rng = np.random.default_rng(52)
+    bf = lambda a: to_dev(wl.f32_to_bf16_bits(a.astype(np.float32)))
+    attn, stream = bf(rng.standard_normal((T, H))), bf(3 * rng.standard_normal((T, H)))
+    w1, w2 = bf(1 + 0.1 * rng.standard_normal(H)), bf(1 + 0.1 * rng.standard_normal(H))
+    w_router = to_dev((rng.standard_normal((E, H)) * H ** -0.5).astype(np.float32))
+    y, h = moe.moe_rmsnorm(attn, w1, residual=stream)
+    logits = y.float() @ w_router.t()
+    q, sc = moe.moe_quantize_fp8(y, 128)
+    outs = [moe.moe_layer_decode(y, logits, k, layer.up_p, layer.down_p),
+            moe.moe_layer_decode(q, logits, k, layer.up_p, layer.down_p, x_scales=sc)]
+    idx_o, w_o = _route64(to_host(logits), k)
+    q64 = q.float().cpu().numpy().astype(np.float64) * np.repeat(to_host(sc).astype(np.float64), 128, axis=1)
+    for (out, idx, _), x64, fp8 in zip(outs, (_out64(y), q64), (False, True)):
+        assert (to_host(idx) == idx_o).all()
+        _check(out, *_reference(layer, x64, idx_o, w_o, fp8))
+        y2, h2 = moe.moe_rmsnorm(out, w2, residual=h)
+        s64 = _out64(h) + _out64(out)
+        assert (np.abs(_out64(h2) - s64) <= (2.0 ** -8 + U) * np.abs(s64)).all()
+        v = _out64(h2)
+        n = v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6) * _out64(w2)
+        assert (np.abs(_out64(y2) - n) <= (2.0 ** -8 + 200 * U) * np.abs(n)).all()

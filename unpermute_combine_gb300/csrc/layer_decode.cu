@@ -23,9 +23,14 @@
 // The issuing threads are elected (elect_one): one token, 2 of 64 experts,
 // H = 4096, I = 2048: 34.4 us against 39.5 behind a test of the lane.  Where
 // memory is the bound throughout it costs 1 to 2% (the last case below).
+// What bounds many tokens of an expert (64 tokens, 8 of 8 experts, H = 4096, I = 2048:
+// 95 us, weights 60): every tile of weight rows brings its own copy of the unit's
+// token rows, half as many bytes again as the weights, or as many in the down phase
+// and for e4m3 rows, which come in two parts; and the rows leave the ring 3 or 4 stages.
 // Precision: the MMA's operands are bf16, but a hidden value, and an e4m3 code
 // times its scale, are not bf16 values.  Both are split into a bf16 value and
-// the bf16 value of the rest (16 bits together), which stand side by side as
+// the bf16 value of the rest (16 bits together, off by 2^-17 at most, where the output
+// is rounded to 2^-8), which stand side by side as
 // columns of one B tile; the epilogue adds the two columns.  An MMA this narrow
 // takes as long as the read of its A tile (37 cycles measured, a fifth of the
 // time that the tile takes to arrive), so the second part costs next to nothing.
@@ -35,11 +40,12 @@
 // so a block's ring fills with down projections while it waits.
 // Every block works the routing out for itself (top-k, softmax, each expert's
 // tokens) in shared memory: a launch of its own would take longer.
-// Measured (one call after another in a CUDA graph, other weights each time): one
-// token, 6 of 64 experts, H = 2048, I = 1408: 32.5 us, of which 10 + 4 stream the
-// weights; the rest is latency (routing 4 us, the two meetings, the last sum).
-// 16 tokens of these: 130 us, 6.2 TB/s; 64 tokens over 256 experts, H = 7168,
-// I = 2048: 2.88 ms, 6.8 TB/s (a copy on the same GPU: 6.7).  Three launches, with
+// Measured (one call after another in a CUDA graph, other weights each time; the GPUs
+// differ by up to 4%, and calls from Python take 1 to 4% more): one token, 6 of 64
+// experts, H = 2048, I = 1408: 32.5-33.0 us, of which 10 + 4 stream the weights; the
+// rest is latency (routing 4 us, the two meetings, the last sum).  16 tokens of
+// these: 129-131 us, 6.2 TB/s; 64 tokens over 256 experts, H = 7168, I = 2048:
+// 2.82-2.88 ms, 6.8 TB/s (a copy on the same GPU: 6.7).  Three launches, with
 // the down projections' overlapping the up projections', were as fast for one token
 // and slower in between (139 us for the 16 tokens, where one launch had 132): each
 // launch worked the routing out anew.  Dot products by warps, without tensor cores: 82 us, 439 us, 12.2 ms.
@@ -992,6 +998,9 @@ layer_kernel(const __grid_constant__ CUtensorMap map_up, const __grid_constant__
                         if (col < m.cols) {
                             uint16_t* hp = a.hidden + int64_t(m.first + c0 + c1) * a.I + m.col + col;
                             float h[4];
+                            // silu by the fast exponential and quotient, as in the grouped
+                            // layer: off by some 2^-22 and |g| 2^-24, below the 2^-17 that the
+                            // row is kept to
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const float other = ex[(c1 + c) * 64], g = gate ? v[c] : other;

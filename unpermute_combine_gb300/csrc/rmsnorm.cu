@@ -259,8 +259,9 @@ struct NormArgs {
 // A row to blockDim.x threads (a warp, blockDim.y rows a block; or the block), V
 // chunks a thread held in registers between the two passes over the row.  Bound
 // by memory: 16384 rows of 7168 in bf16 with a residual take 136 us, 6.9 TB/s (a
-// copy: 6.7); with e4m3 output 156 us, 5.3 TB/s, where the instructions of the
-// quantization fill 60% of the issue slots; rows of 7001 elements 150 us.  64
+// copy: 6.7); with e4m3 output 156 us, 5.3 TB/s, where 71% of the issue slots are
+// taken (290 warp instructions for 8 elements of each lane, against 145 without the
+// quantization; the divisions by a.lanes are some of them); rows of 7001 elements 150 us.  64
 // registers where a thread has 64 bytes: with 76, the e4m3 form took 176 us.
 template <typename X, typename W, int V, bool kQuant, bool kShift>
 __global__ void __launch_bounds__(V >= 4 ? kMaxThreads / 2 : kMaxThreads, V == 4 ? 2 : 1)
@@ -356,7 +357,8 @@ rmsnorm_kernel(const NormArgs a) {
 }
 
 // The same for tensors that do not start on a 16-byte boundary: elements
-// threadIdx.x, + blockDim.x, ..., eight of them a thread, in registers.
+// threadIdx.x, + blockDim.x, ..., eight of them a thread, in registers.  Bound by loads
+// of single elements: 16384 rows of 7168 in bf16 405 us.
 template <typename X, typename W>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_odd_kernel(const NormArgs a) {
@@ -477,9 +479,12 @@ __host__ __device__ constexpr uint32_t slot_size(int64_t H, bool three) {
 // while a row waits for its sums; V chunks a thread.  The columns' shares of grad_weight stay in registers over all rows of
 // the block; its teams' shares are added up at the end, in order, and the blocks'
 // by rmsnorm_grad_weight_kernel.
-// Bound by memory on long batches (16384 rows of 7168 in bf16 with grad_h: 145 us,
+// Bound by memory on long batches (16384 rows of 7168 in bf16 with grad_h: 144 us,
 // 6.5 TB/s), by the way in and out of the ring on short ones (4096 rows of 2048, 3.4
-// rows a team: 22 us with the second launch, of which 10 move the bytes).  One row a
+// rows a team: 22 us with the second launch, of which 10 move the bytes).  Shifted rows
+// (7172 wide: 184 us) pay a barrier more and the repair of their edges before a row's
+// sums.  float32 rows of 12000, whose grad_h is loaded when it is added: 150 us for 4096,
+// memory 118 (8528, with grad_h in the ring: 88, memory 84).  One row a
 // block at a time, without a ring: 295 and 44 us.  Packed float instructions and
 // fewer shuffles: no faster, though 70% of the issue slots are taken.
 template <typename X, typename W, int V, bool kShift>
@@ -674,7 +679,8 @@ rmsnorm_backward_kernel(const BwdArgs a, uint32_t* status) {
 }
 
 // Tensors that do not start on a 16-byte boundary: elements threadIdx.x, +
-// blockDim.x, ..., eight of them a thread; the next row's are loaded while this one's are worked on.
+// blockDim.x, ..., eight of them a thread; the next row's are loaded while this one's are
+// worked on.  Bound by loads of single elements: 16384 rows of 7168 in bf16 610 us.
 template <typename X, typename W>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_backward_odd_kernel(const BwdArgs a) {
@@ -735,7 +741,9 @@ rmsnorm_backward_odd_kernel(const BwdArgs a) {
 
 // Rows too long for the registers or the ring.  The block's share of grad_weight
 // lives in its row of `partial`: every column is read and written by one thread
-// only.
+// only.  Bound by reading every row twice, element by element, and the share with it:
+// 4096 rows of 16384 in bf16 443 us, of 20000 in float32 605, three and five times what
+// the bytes take.
 template <typename X, typename W>
 __global__ void __launch_bounds__(kMaxThreads)
 rmsnorm_backward_long_kernel(const BwdArgs a) {
