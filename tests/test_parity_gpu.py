@@ -642,3 +642,77 @@ def test_pipeline_skewed_sampled():
                                                sp_local, w_o)
     assert (to_host(g["gy"][torch.from_numpy(rows).long().cuda()]) == gy_o).all()
     assert within_one_bf16_ulp(to_host(g["gp"])[toks], gp64).all()
+
+
+@pytest.mark.parametrize("warm", [True, False])
+@pytest.mark.parametrize("between", ["nothing", "zeros", "noise", "the same image", "an eager call",
+                                     "the layer's meeting"])
+@pytest.mark.parametrize("T,E,k", [(4096, 256, 8), (300, 64, 6)])
+def test_route_replayed_with_other_logits(T, E, k, between, warm):
+    """A captured route repeats its barrier's tag: what a replay leaves in the workspace,
+    or what another writer puts there after every replay, must not let the next one
+    through before all blocks have counted.  Every replay has other logits."""
+    rng = np.random.default_rng(T)
+    hot = rng.permutation(E)
+    sets = []
+    for i in range(6):                                     # the experts' shares move about
+        lg = (rng.standard_normal((T, E)) + 3.0 * (hot == 0)[None, :] * (i % 2)
+              + np.roll(np.linspace(0, 2, E), 40 * i)[None, :]).astype(np.float32)
+        sets.append((to_dev(lg), oracle.route(lg, k)))
+    nbytes = moe.moe_route_workspace_size(T, E, k)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ws = torch.randint(0, 256, (nbytes,), dtype=torch.uint8, device="cuda", generator=gen)
+    image = ws.clone()
+    lg = sets[0][0].clone()
+    moe.moe_device_status()
+    if warm:
+        moe.moe_route(lg, k, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = moe.moe_route(lg, k, workspace=ws, routing_map=True)
+    for turn, (logits, o) in enumerate(sets + sets[::-1]):
+        lg.copy_(logits)
+        for t in (r.counts, r.offsets, r.sorted_indices, r.slot_pos):
+            t.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        _assert_route_equal(r, o, E)
+        assert moe.moe_workspace_status(ws) == 0 and moe.moe_device_status() == 0
+        if between == "zeros":
+            ws.zero_()
+        elif between == "noise":
+            ws.copy_(torch.randint(0, 256, (nbytes,), dtype=torch.uint8, device="cuda", generator=gen))
+        elif between == "the same image":
+            ws.copy_(image)
+        elif between == "an eager call":
+            e = moe.moe_route(sets[turn % 6][0], k, workspace=ws, routing_map=True)
+            _assert_route_equal(e, sets[turn % 6][1], E)
+        elif between == "the layer's meeting":
+            ws[:4096].fill_(turn & 1)
+
+
+def test_route_replays_back_to_back():
+    """Replays of two graphs over one workspace with nothing waited for in between: the
+    last ones' results are the oracle's."""
+    T, E, k = 2000, 128, 8
+    rng = np.random.default_rng(9)
+    ws = torch.zeros(moe.moe_route_workspace_size(T, E, k), dtype=torch.uint8, device="cuda")
+    pairs = []
+    for i in range(2):
+        lg = (rng.standard_normal((T, E)) + np.roll(np.linspace(0, 3, E), 60 * i)[None, :]).astype(np.float32)
+        d = to_dev(lg)
+        moe.moe_route(d, k, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            r = moe.moe_route(d, k, workspace=ws, routing_map=True)
+        pairs.append((graph, r, oracle.route(lg, k), d))       # (a graph reads d where it is)
+    moe.moe_device_status()
+    for _ in range(50):
+        for graph, _, _, _ in pairs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, r, o, _ in pairs:
+        _assert_route_equal(r, o, E)
+    assert moe.moe_device_status() == 0

@@ -396,12 +396,17 @@ struct PlaceOut {
     WsHeader* header;
     uint32_t* counter;          // grid-barrier count (workspace): arrivals, then departures
     uint32_t* go;               // [2] this call's way, published by block 0 (tag: count,
-                                // tag ^ 1: flags), 8 bytes after the count: one load reads both
-    uint64_t* marker;           // tag of the last call whose blocks all left the barrier
-    uint64_t* flags;            // [G] arrival flags, for a workspace in an unknown state
+                                // tag ^ 1: flags), 8 bytes after the count: one load reads both;
+                                // after the call the same ^ 2
+    uint64_t* marker;           // tag ^ 2 of the last call whose blocks all left the barrier
+    uint64_t* flags;            // [G] for a workspace in an unknown state: tag, here; tag ^ 1, gone
     uint64_t tag;               // this call's tag (distinct for every call in the process)
-    uint64_t expect;            // the marker a clean workspace holds (the previous call's tag)
+    uint64_t expect;            // the marker a clean workspace holds (the previous call's)
 };
+
+// What a call leaves in the marker, and in `go` (the way's last bit aside): no value that a
+// call with the same tag, a replay of it in a graph, would take for its own.
+constexpr uint64_t kDone = 2u;
 
 // The placement of route_fast_place_kernel inside the fused route, from this
 // block's shared memory: wait until every block has written its count row
@@ -423,10 +428,10 @@ __device__ void place_from_block(const uint16_t* __restrict__ hist, int E, int k
     const int64_t t0 = int64_t(b) * tpb;
     const int nt = int(max64(0, min64(tpb, T - t0)));
     // The grid barrier, without clearing the workspace between calls.  Block 0
-    // loaded the count and the marker (the tag of the last call whose blocks
-    // all left the barrier) when it started, before any block of this call
+    // loaded the count and the marker (of the last call whose blocks all left
+    // the barrier) when it started, before any block of this call
     // could arrive, and published the way in the word `go` after its top-k:
-    // this call's tag for the count (the marker held the tag of the previous
+    // this call's tag for the count (the marker held that of the previous
     // call on this workspace and the count was zero), the tag ^ 1 for the
     // flags.  (With the marker alone, a write over the count that left the
     // marker intact would let blocks through before every row is written.)
@@ -435,16 +440,22 @@ __device__ void place_from_block(const uint16_t* __restrict__ hist, int E, int k
     // at GPU scope), then reads `go` and the count together:
     //  - count: done once all G blocks have arrived.  Leaving, each block adds
     //    1 more, and the last of the 2G resets the count to zero and stores
-    //    the tag in the marker.
+    //    the tag ^ kDone in `go` and the marker.
     //  - flags (a new workspace, other data written over it or over its
     //    count, a call that timed out): the block stores the tag in its own
     //    flag and warp 0 polls the G flags until all hold it -- correct
     //    whatever the workspace held, as a foreign flag or `go` matches only
-    //    by a 2^-63 chance.  Block 0 then takes *s_count0 (the count it
-    //    found) plus G off the count -- zero once every arrival has landed,
-    //    in whatever order -- and stores the marker.  (Should an arrival have
-    //    come before block 0 read the count, the count ends nonzero and the
-    //    next call takes the flags again, which clears it.)
+    //    by a 2^-62 chance.  Leaving, a block flips its flag's last bit (a
+    //    flag that is still polled counts either way); block 0 also takes
+    //    *s_count0 (the count it found) plus G off the count -- zero once
+    //    every arrival has landed, in whatever order.  (Should an arrival
+    //    have come before block 0 read the count, the count ends nonzero and
+    //    the next call takes the flags again, which clears it.)  When block 0
+    //    has placed its slots and every other block has left, it clears the
+    //    flags and stores `go` and the marker.
+    // A replayed graph repeats a call with its tag: neither `go` nor a flag
+    // may be left as that call would take them, or it passes the barrier
+    // before the other blocks have written their rows.
     // (A memset of the count before every call measured 1.9 us per call; a
     // self-initialising compare-and-swap count was 90 us slower.)
     __shared__ int s_ok, s_way;
@@ -484,7 +495,7 @@ __device__ void place_from_block(const uint16_t* __restrict__ hist, int E, int k
                 uint64_t v;
                 asm volatile("ld.acquire.gpu.global.u64 %0, [%1];"
                              : "=l"(v) : "l"(po.flags + i) : "memory");
-                mine = mine && v == po.tag;
+                mine = mine && (v | 1u) == (po.tag | 1u);
             }
             if (__all_sync(kFull, mine)) break;
             const bool late = global_ns() - start > kWaitLimitNs;
@@ -502,12 +513,15 @@ __device__ void place_from_block(const uint16_t* __restrict__ hist, int E, int k
         if (s_way == 1) {
             if (atomicAdd(po.counter, 1u) == 2u * uint32_t(G) - 1u) {
                 *po.counter = 0u;
-                *po.marker = po.tag;
+                *reinterpret_cast<uint64_t*>(po.go) = po.tag ^ kDone;
+                *po.marker = po.tag ^ kDone;
             }
-        } else if (b == 0) {
+        } else {
+            // (an atomic operation keeps what the flag's store released with it)
+            asm volatile("red.relaxed.gpu.global.xor.b64 [%0], %1;"
+                         :: "l"(po.flags + b), "l"(uint64_t(1)) : "memory");
             // the count is *s_count0 plus the G arrivals, whenever they land
-            atomicSub(po.counter, *s_count0 + uint32_t(G));
-            *po.marker = po.tag;
+            if (b == 0) atomicSub(po.counter, *s_count0 + uint32_t(G));
         }
     }
     // rows of 16-bit counts, summed as packed pairs (every sum is at most
@@ -584,6 +598,32 @@ __device__ void place_from_block(const uint16_t* __restrict__ hist, int E, int k
         po.slot_pos[t0 * k + i] = pos;
         po.sorted_indices[pos] = int32_t(t0 + tk);
         if (po.permuted_probs) po.permuted_probs[pos] = s_w[i];
+    }
+    if (s_way == 2 && b == 0 && threadIdx.x < 32) {
+        const uint64_t start = global_ns();
+        bool gone = false;
+        for (;;) {
+            bool mine = true;
+            for (int i = int(threadIdx.x); i < G; i += 32) {
+                uint64_t v;
+                asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];"
+                             : "=l"(v) : "l"(po.flags + i) : "memory");
+                mine = mine && v == (po.tag ^ 1u);
+            }
+            gone = __all_sync(kFull, mine);
+            if (gone) break;
+            const bool late = global_ns() - start > kWaitLimitNs;
+            if (__any_sync(kFull, late)) break;
+            __nanosleep(32);
+        }
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        __syncwarp();
+        for (int i = int(threadIdx.x); i < G; i += 32) po.flags[i] = 0u;
+        if (threadIdx.x == 0) {
+            *reinterpret_cast<uint64_t*>(po.go) = po.tag ^ 1u ^ kDone;
+            if (gone) *po.marker = po.tag ^ kDone;
+            else if (dev_status) atomicExch(dev_status, uint32_t(MOE_ERR_TIMEOUT));
+        }
     }
 }
 
@@ -1163,8 +1203,8 @@ moe_status_t launch_topk_k(const float* logits, int64_t T, int E, int k, int tpb
 // process (the SplitMix64 output function -- Steele, Lea and Flood, "Fast
 // splittable pseudorandom number generators", OOPSLA 2014 -- of a call
 // counter: its odd Weyl step and xor-shift-multiply mix are bijections of
-// 64-bit words), and the tag the previous call on the same workspace
-// received, which the workspace's marker holds if that call completed.
+// 64-bit words), and what the previous call on the same workspace leaves in
+// the workspace's marker if it completes.
 void barrier_tags(const void* workspace, uint64_t* tag, uint64_t* expect) {
     static std::mutex m;
     static std::map<std::pair<int, const void*>, uint64_t> last;
@@ -1180,7 +1220,7 @@ void barrier_tags(const void* workspace, uint64_t* tag, uint64_t* expect) {
     const auto it = last.find(key);
     *expect = it != last.end() ? it->second : ~*tag;    // unknown workspace: no match
     if (it == last.end() && last.size() >= 4096) last.clear();
-    last[key] = *tag;
+    last[key] = *tag ^ kDone;
 }
 
 // The few-threads-a-token top-k (TPT threads a token, NG groups of 8
