@@ -493,7 +493,8 @@ moe_status_t moe_permute_quantize_fp8(const void* x, int64_t T, int64_t H, int b
  * moe_rmsnorm_quantize_fp8: the same norm with the output quantized as
  * moe_quantize_fp8 does, from the float32 values (not from bf16 ones): per
  * block of `block` (32, 64, 128 or 256) elements scale = amax / 448 (1 for an
- * all-zero block) and x_q = e4m3(y / scale), of the rounded float quotient.
+ * all-zero block, and never below 2^-149) and x_q = e4m3(y / scale), of the
+ * rounded float quotient.
  * x_q [T,H] e4m3 bytes, scales [T, H/block] float.  H a multiple of block (else
  * MOE_ERR_INVALID_ARG) and at most 32768 (else MOE_ERR_UNSUPPORTED); x, residual,
  * weight and residual_out 16-byte, x_q 8-byte, scales 4-byte aligned (else

@@ -572,3 +572,20 @@ def test_wide_float32_rows_between_others(T, H):
     assert (np.abs(_val(gw) - gw64) <= (D / 2 + 10 + T) * U * gw_size).all()
     for b in big:
         assert torch.isnan(b[:64]).all() and torch.isnan(b[64 + T * H:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_of_the_smallest_floats(dtype):
+    """Blocks whose largest value is below 448 times the smallest float: the scale is the
+    smallest float, not 0, and a 0 in them stays 0."""
+    H, block = 256, 32
+    k = np.arange(H) % block
+    w = (k * np.repeat([1, 2, 4, 7, 1, 3, 5, 7], block)).astype(np.float64)      # at most 217
+    w[4 * block:5 * block] = 0.0
+    w[4 * block] = 1.0
+    w[1::2] *= -1
+    ones = to_dev(wl.as_activation(np.ones((3, H), np.float32), dtype))
+    q, sc, _ = moe.moe_rmsnorm_quantize_fp8(ones, to_dev((w * 2.0 ** -149).astype(np.float32)), eps=0.0,
+                                            block=block)
+    assert (to_host(sc) == np.float32(2.0 ** -149)).all()
+    assert torch.equal(q.float().cpu(), torch.from_numpy(w).to(torch.float8_e4m3fn).float().expand(3, H))

@@ -342,10 +342,11 @@ rmsnorm_kernel(const NormArgs a) {
                 }
                 for (int o = a.lanes >> 1; o > 0; o >>= 1)
                     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                // amax / 448: the product with 1/448, and its remainder put back
+                // amax / 448: the product with 1/448, and its remainder put back; no scale
+                // is 0, by which a 0 beside the smallest floats would become NaN
                 float s = amax * (1.0f / 448.0f);
                 s = fmaf(fmaf(s, -448.0f, amax), 1.0f / 448.0f, s);
-                if (!(s >= 0x1p-126f)) s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+                if (!(s >= 0x1p-126f)) s = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-149f) : 1.0f;
                 if (c < chunks) {
                     uint2* q = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.H);
                     q[c] = q8(y, s);
