@@ -477,9 +477,9 @@ __host__ __device__ constexpr uint32_t slot_size(int64_t H, bool three) {
 // Rows in teams of blockDim.x threads, blockDim.y teams a block.  A team has a ring
 // of rows in shared memory (h, grad_y and grad_h of each, or the first two where only
 // they have room twice), which bulk copies fill rows ahead, so that reading goes on
-// while a row waits for its sums; V chunks a thread.  The columns' shares of grad_weight stay in registers over all rows of
-// the block; its teams' shares are added up at the end, in order, and the blocks'
-// by rmsnorm_grad_weight_kernel.
+// while a row waits for its sums; V chunks a thread.  The columns' shares of
+// grad_weight stay in registers over all rows of the block; its teams' shares are
+// added up at the end, in order, and the blocks' by rmsnorm_grad_weight_kernel.
 // Bound by memory on long batches (16384 rows of 7168 in bf16 with grad_h: 144 us,
 // 6.5 TB/s), by the way in and out of the ring on short ones (4096 rows of 2048, 3.4
 // rows a team: 22 us with the second launch, of which 10 move the bytes).  Shifted rows
