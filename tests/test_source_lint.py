@@ -26,3 +26,16 @@ def test_no_warp_collective_behind_a_short_circuit():
             if pat.search(line):
                 bad.append(f"{os.path.basename(path)}:{n}: {line.strip()}")
     assert not bad, "warp collective behind ||, && or ?:\n" + "\n".join(bad)
+
+
+def test_no_load_is_multicast():
+    """A TMA load that fills several blocks' shared memory may only read the memory of its
+    own GPU, which the addresses that a caller gives do not say.  A commit, which multicasts
+    an arrival and reads nothing, is not meant."""
+    bad = []
+    for path in SOURCES:
+        text = re.sub(r'"\s*\n?\s*"', "", open(path).read())       # adjacent string literals
+        for copy in re.findall(r"cp\.async\.bulk[^;\"]*", text):
+            if "multicast" in copy:
+                bad.append(f"{os.path.basename(path)}: {copy.strip()}")
+    assert not bad, "load with cluster multicast:\n" + "\n".join(bad)

@@ -191,16 +191,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         tma_load_2d(dst, map, c0, c1, bar);
 }
 
-// The same to both blocks of a pair, each of which the leader's barrier counts.
-__device__ __forceinline__ void load_tile_both(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                               uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar),
-           "h"(uint16_t(3)) : "memory");
-}
-
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, int c0, int c1, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  :: "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(src) : "memory");
@@ -507,13 +497,10 @@ grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
                                        CTAS * (kTileBytes + parts * S::kScales));
             load_tile<CTAS>(st + S::kWeights, &maps.b, ks * kRowBytes,
                             int(at.e * args.N) + at.n * BN + rank * 128, fb);
-            // (each block of a pair brings one half of the columns' scales for both)
-            if (rank < parts) {
-                const uint32_t dst = st + S::kWeightScales + rank * S::kScales;
-                const int chunk = ((at.e * nb_all + nb + rank) * k_stages + ks) * S::kParts;
-                if (CTAS == 2) load_tile_both(dst, &maps.w_scales, 0, chunk, fb);
-                else load_tile<1>(dst, &maps.w_scales, 0, chunk, fb);
-            }
+            // (each block of a pair has the scales of all the tile's columns)
+            for (int h = 0; h < parts; ++h)
+                load_tile<CTAS>(st + S::kWeightScales + h * S::kScales, &maps.w_scales, 0,
+                                ((at.e * nb_all + nb + h) * k_stages + ks) * S::kParts, fb);
         };
         auto load_rows = [&](int ks, uint32_t i) {
             const int rows = rows_of(at, rank), row = at.row + rank * BM;
