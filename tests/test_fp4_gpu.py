@@ -492,3 +492,22 @@ def test_elements_past_32_bits():
                                     torch.tensor([0, 300], dtype=torch.int32, device="cuda"), 16)
     # one step of 64 columns: the same sum, rounded once
     assert torch.equal(y[tail], yt)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("K", [32, 256, 512, 1024, 1280, 1536, 2592])
+def test_pairs_with_fewer_and_more_stages_than_the_ring(K, block):
+    """One to eleven stages a tile: which stages' last arrivals no next stage waits for differs.
+    Calls in a row end and begin on the same SMs."""
+    M, E, N = 20000, 2, 4096
+    xq, xs, x = fp4_rows(M, K, block, K)
+    wq, ws, g, w = fp4_weights(E, N, K, block, K + 1)
+    off = torch.tensor([0, 9001, M], dtype=torch.int32, device="cuda")
+    out = [moe.moe_grouped_matmul_fp4(xq, xs, wq, ws, off, block, alpha=g) for _ in range(20)]
+    for y in out:
+        assert moe.moe_workspace_status(y._moe_workspace) == 0
+        assert torch.equal(y.view(torch.int16), out[0].view(torch.int16))
+    for e, (a, b) in enumerate(((0, 9001), (9001, M))):
+        al = 1.0 if g is None else g[e].double()
+        want, tol = x[a:b] @ w[e].t() * al, product_error(x[a:b], w[e], K) * al
+        assert ((out[0][a:b].double() - want).abs() <= want.abs() * 2.0 ** -8 + tol).all()

@@ -536,11 +536,20 @@ grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
                 load_rows(ks, it);
             }
         }
-        if (s_failed && rank == 0)  // copies in flight land before the blocks end
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+        // The last stages' commits arrive here too, which no next stage waits for, and nothing may
+        // arrive at a block that has ended.
+        const uint32_t last = it > kStages ? it - kStages : 0;
+        for (uint32_t i = last; i < it && !s_failed; ++i)
+            if (!mbar_wait(smem_addr(&empty_bar[i % kStages]), parity(i))) s_failed = 1;
+        if (s_failed && rank == 0) {  // copies in flight land before the blocks end
+            for (uint32_t i = last; i < it; ++i)
                 mbar_wait(smem_addr(&full_bar[i % kStages]), parity(i));
-        else if (s_failed)          // (the other block's have no barrier here: a millisecond)
+        } else if (s_failed) {
+            // the leader's last commit, behind its MMAs, and copies, which have no barrier
+            // here: a millisecond
+            mbar_wait(smem_addr(&drain_bar), 0);
             for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000;) __nanosleep(1000);
+        }
     } else if (warp == 1 && rank == 0 && elect_one()) {
         // ------------------------------------------------------ MMAs
         // The one thread's own instructions are what bounds a pair's stage of few MMAs, so
