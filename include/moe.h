@@ -632,8 +632,9 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  * with half the bytes of FP8.  Codes: 1 sign, 2 exponent, 1 mantissa bit (0, 0.5, 1,
  * 1.5, 2, 3, 4, 6), two to a byte, the element of even index in the low half.
  *   block = 16: one e4m3 byte a block, scale = e4m3(amax / (6 g)) to nearest even,
- *     saturated at 448; g = *global_scale, a positive finite float on the device for
- *     the whole tensor (NULL: 1), e.g. its largest magnitude / (448 * 6)
+ *     saturated at 448; g = *global_scale, a float on the device for the whole tensor
+ *     (NULL: 1), e.g. its largest magnitude / (448 * 6): not negative, 6 g finite.  A
+ *     block of zeros has the scale 0 with any g, 0 among them
  *   block = 32: one exponent byte b a block, scale = 2^(b - 127) =
  *     2^(floor(log2 amax) - 2), b >= 0; no g (global_scale NULL, else
  *     MOE_ERR_INVALID_ARG)

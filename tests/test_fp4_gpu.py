@@ -511,3 +511,65 @@ def test_pairs_with_fewer_and_more_stages_than_the_ring(K, block):
         al = 1.0 if g is None else g[e].double()
         want, tol = x[a:b] @ w[e].t() * al, product_error(x[a:b], w[e], K) * al
         assert ((out[0][a:b].double() - want).abs() <= want.abs() * 2.0 ** -8 + tol).all()
+
+
+# --------------------------------------------- zeros, and the g that they give
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_zeros_without_a_global_scale(dtype):
+    """g = largest / (448 * 6) of a tensor of zeros is 0: its blocks are 0, not NaN."""
+    x = torch.zeros((3, 96), dtype=dtype, device="cuda")
+    g = scalar(0.0)
+    q, sc = moe.moe_quantize_fp4(x, 16, global_scale=g)
+    assert not q.any() and not sc.any()
+    assert not moe.moe_dequantize_fp4(q, sc, 16, global_scale=g).any()
+    slot = torch.arange(6, dtype=torch.int32, device="cuda").view(3, 2)
+    q, sc = moe.moe_permute_quantize_fp4(x, slot, 16, global_scale=g)
+    assert not q.any() and not sc.any()
+    x[1, 40], x[2, 3] = float("nan"), 2.0           # NaN stays NaN; scale g is 0: code 0
+    q, sc = moe.moe_quantize_fp4(x, 16, global_scale=g)
+    want = torch.zeros_like(sc)
+    want[1, 2], want[2, 0] = 0x7F, 0x7E
+    assert torch.equal(sc, want) and not q.any()
+
+
+def test_an_expert_of_zeros():
+    """Packed with one g an expert, its rows' products are 0 and the others' as without it."""
+    M, E, N, K = 30, 3, 128, 96
+    w = rows(E * N, K, 1, scale=K ** -0.5).view(E, N, K)
+    w[1] = 0.0
+    g = w.float().abs().amax((1, 2)) / (448 * 6)
+    assert g[1].item() == 0.0
+    wq, ws = moe.moe_pack_fp4(w, 16, global_scale=g)
+    assert not wq[1].any() and not ws.view(E, -1)[1].any()
+    xq, xs, _ = fp4_rows(M, K, 16, 2)
+    off = torch.tensor([0, 10, 20, 30], dtype=torch.int32, device="cuda")
+    y = moe.moe_grouped_matmul_fp4(xq, xs, wq, ws, off, 16, alpha=g)
+    assert not y[10:20].any() and torch.isfinite(y).all()
+    for e in (0, 2):
+        cut = slice(10 * e, 10 * e + 10)
+        alone = moe.moe_grouped_matmul_fp4(
+            xq[cut].contiguous(), xs[cut].contiguous(), wq[e:e + 1], ws.view(E, -1)[e].contiguous(),
+            torch.tensor([0, 10], dtype=torch.int32, device="cuda"), 16, alpha=g[e:e + 1])
+        assert torch.equal(y[cut], alone) and alone.any()
+
+
+@pytest.mark.parametrize("zero", ["up", "down", "both"])
+def test_a_network_of_zeros(zero):
+    M, E, H, I = 20, 2, 128, 64
+    w_up, w_down = rows(E * 2 * I, H, 3).view(E, 2 * I, H), rows(E * H, I, 4).view(E, H, I)
+    if zero != "down":
+        w_up[0] = 0.0
+    if zero != "up":
+        w_down[0] = 0.0
+    gu, gd = (w.float().abs().amax((1, 2)) / (448 * 6) for w in (w_up, w_down))
+    up, down = moe.moe_pack_fp4(w_up, 16, global_scale=gu, gate_up=True), \
+        moe.moe_pack_fp4(w_down, 16, global_scale=gd)
+    xq, xs, _ = fp4_rows(M, H, 16, 5)
+    off = torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda")
+    # hidden rows of zeros alone, and their g, which is 0 then
+    for hs in (scalar(0.01), None) if zero == "down" else (scalar(0.01), scalar(0.0), None):
+        y = moe.moe_grouped_swiglu_fp4(xq, xs, *up, *down, off, 16, alpha_up=gu, alpha_down=gd,
+                                       hidden_scale=hs)
+        assert not y[:10].any() and torch.isfinite(y).all()
+        assert y[10:].any() or (hs is not None and hs.item() == 0.0)

@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t fp4_scale(uint32_t amax, const Fp4Unit& u, f
     }
     const float a = __uint_as_float(amax);
     float q = __fmul_rn(a, u.inv_six);
-    if (!u.normal) q = __fdiv_rn(a, u.six);
+    if (!u.normal) q = amax ? __fdiv_rn(a, u.six) : 0.0f;       // (zeros may have a g of 0)
     else if (q < 1024.0f) q = quotient(a, u.six, u.inv_six);    // above, it saturates
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(q));
