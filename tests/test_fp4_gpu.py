@@ -573,3 +573,21 @@ def test_a_network_of_zeros(zero):
                                        hidden_scale=hs)
         assert not y[:10].any() and torch.isfinite(y).all()
         assert y[10:].any() or (hs is not None and hs.item() == 0.0)
+
+
+@pytest.mark.parametrize("block,g", [(16, None), (16, 0.0237), (16, 1e-33), (32, None)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_negative_zeros_keep_their_sign(dtype, block, g):
+    """The code of -0 / step is that of -0, as is that of what lies below 1/4 of a step."""
+    x = rows(5, 96, 17, dtype).float() * (1.0 if g is None else g * 100)
+    x[:, 1::4], x[:, 3::8] = -0.0, 0.0
+    x[1, 5::8], x[2, 5::8] = -1e-45, -1e-40
+    x = x.to(dtype)
+    codes, byte, _ = f4.quantize(x, block, 1.0 if g is None else g)
+    assert (codes == 8).any()
+    q, sc = moe.moe_quantize_fp4(x, block, global_scale=scalar(g))
+    assert torch.equal(sc, byte) and torch.equal(f4.unpairs(q), codes)
+    w = x.to(BF16).view(1, 5, 96)
+    codes, _, _ = f4.quantize(w[0], block, 1.0 if g is None else g)
+    q, _ = moe.moe_pack_fp4(w, block, global_scale=scalar(g))
+    assert torch.equal(f4.unpairs(q[0]), codes)

@@ -70,10 +70,11 @@ __device__ __forceinline__ float quotient(float a, float b, float r) {
     const float q = __fmul_rn(a, r);
     return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
 }
-// Two at once; less = -b.
-__device__ __forceinline__ float2 quotient2(float2 a, float2 less, float2 r) {
-    const float2 q = mul2(a, r);
-    return fma2(fma2(q, less, a), r, q);
+// Two at once, negated: -(a / b), less = -r.  A zero comes out with the sign that -(a / b)
+// has, where the steps as above would make -0 into 0: -0 * r - (-0 * b - a) is 0.
+__device__ __forceinline__ float2 less_quotient2(float2 a, float2 b, float2 less) {
+    const float2 q = mul2(a, less);
+    return fma2(fma2(q, b, a), less, q);
 }
 
 // Scale byte of a block whose largest magnitude has the bits `amax` (they order
@@ -105,6 +106,7 @@ template <int BLOCK, int N>
 __device__ __forceinline__ void fp4_codes(const float* v, uint32_t scale, float step,
                                           uint32_t* out) {
     float q[N];
+    uint32_t sign = 0;          // where q is the negated quotient: the sign bits of eight codes
     if (BLOCK == 32) {          // a power of two: the product with its inverse is the quotient
         const bool nan = scale == kNanScaleE8M0;
         const float2 inv = both(__uint_as_float((254u - scale) << 23));
@@ -113,11 +115,12 @@ __device__ __forceinline__ void fp4_codes(const float* v, uint32_t scale, float 
             const float2 p = mul2(make_float2(v[i], v[i + 1]), inv);
             q[i] = nan ? 0.0f : p.x, q[i + 1] = nan ? 0.0f : p.y;
         }
-    } else if (far_from_ends(step) && scale != kMostScaleE4M3) {   // |v / step| < 7
-        const float2 r = both(__frcp_rn(step)), less = both(-step);
+    } else if (far_from_ends(step) && scale != kMostScaleE4M3) {   // |v / step| <= 9
+        sign = 0x88888888u;
+        const float2 b = both(step), less = both(-__frcp_rn(step));
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const float2 p = quotient2(make_float2(v[i], v[i + 1]), less, r);
+            const float2 p = less_quotient2(make_float2(v[i], v[i + 1]), b, less);
             q[i] = p.x, q[i + 1] = p.y;
         }
     } else {
@@ -125,7 +128,7 @@ __device__ __forceinline__ void fp4_codes(const float* v, uint32_t scale, float 
         for (int i = 0; i < N; ++i) q[i] = step > 0.0f ? __fdiv_rn(v[i], step) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i) out[i] = e2m1x8(q + 8 * i);
+    for (int i = 0; i < N / 8; ++i) out[i] = e2m1x8(q + 8 * i) ^ sign;
 }
 
 // Largest magnitude bits of N floats.
