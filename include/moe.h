@@ -595,7 +595,8 @@ moe_status_t moe_layer_decode_indices(const void* x, const float* x_scales,
  *   (padding) count nowhere.  An empty sequence adds 0 and counts in S.
  *   loss [2] float, counts [S,E] int32, mean_scores [S,E] float: written completely.
  * Logits of -inf are experts that are off: score 0, gradient 0; a token of nothing
- * else has no scores and adds nothing to either loss (its choices count).  The same
+ * else has no scores and adds nothing to either loss (its choices count).  A logit of
+ * +inf is a sigmoid of 1; the softmax and the z loss of its token are NaN.  The same
  * inputs give the same bits.  Choices outside [-1, E) are not counted, offsets are
  * clamped into [0, T]; either, or offsets that decrease (then the outputs mean
  * nothing), leaves MOE_ERR_DEVICE_CHECK in the workspace status.

@@ -327,3 +327,32 @@ def test_sequences_of_one_token(score):
     if score == "sigmoid":
         d = d * torch.sigmoid(-v)
     assert ((grad.double() - d).abs() <= 0.5 / T * p * E * 8 * rel).all()
+
+
+def test_infinite_logits_of_sigmoids():
+    """sigmoid(inf) is 1: without a z loss nothing of the row is NaN, and without weight for it."""
+    T, E, k = 70, 12, 2
+    x = torch.randn((T, E), generator=gen(23), device="cuda")
+    idx = choices(x, k, 1)
+    x[3, 5], x[40, 2:4], x[41] = INF, INF, INF
+    x[40, 7] = -INF
+    off = torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda")
+    loss, counts, mean = moe.moe_balance_loss(x, idx, off, "sigmoid", 0.5, 0.0)
+    v = x.double()
+    p = torch.sigmoid(v) / torch.sigmoid(v).sum(1, keepdim=True)
+    rel = relative(x)
+    ones = torch.tensor([1.0, 0.0], device="cuda")
+    total = 0.0
+    for s, (a, b) in enumerate(((0, 30), (30, 70))):
+        f = counts[s].double() * E / (k * (b - a))
+        wm = p[a:b].mean(0)
+        assert ((mean[s].double() - wm).abs() <= wm * (rel + 45 * 2.0 ** -24)).all()
+        total += 0.5 / 2 * (f * wm).sum().item()
+        c = f - f.mean()
+        d = 0.5 / 2 / (b - a) * p[a:b] * (c - (p[a:b] * c).sum(1, keepdim=True)) * torch.sigmoid(-v[a:b])
+        bound = 0.5 / 2 / (b - a) * p[a:b] * c.abs().max() * 4 * rel + d.abs() * 2.0 ** -22
+        for gl, zc in ((None, 0.0), (ones, 0.25)):
+            g = moe.moe_balance_loss_backward(x, counts, k, gl, seq_offsets=off, score="sigmoid",
+                                              balance_coef=0.5, z_coef=zc)
+            assert ((g[a:b].double() - d).abs() <= bound).all()
+    assert abs(loss[0].item() - total) <= total * (rel + 2.0 ** -18) and loss[1].item() == 0.0

@@ -505,7 +505,7 @@ balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restr
         for (int i = 0; i < V / 2; ++i) {
             float2 d = mul2(mul2(p.v[i], f), add2(a.v[i], less));
             if (SIGMOID) d = mul2(d, sc.keep.v[i]);
-            d = fma2(sc.u.v[i], zf, d);
+            if (zc != 0.0f) d = fma2(sc.u.v[i], zf, d);    // (an infinite lse times 0 is NaN)
             if (!inside) d = both(0.0f);              // (padding may hold anything)
             row.v[i] = ADD ? add2(d, add.v[i]) : d;
         }
