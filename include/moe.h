@@ -610,7 +610,8 @@ moe_status_t moe_layer_decode_indices(const void* x, const float* x_scales,
  * [T,E] float, e.g. moe_route_backward's (NULL: none), which grad_logits may be
  * itself.  grad_logits [T,E] is written completely: a token outside every sequence
  * gets grad_in or 0.  grad_logits must not overlap logits.  Bad offsets are reported
- * by moe_device_status. */
+ * by moe_device_status, also where no token is in the sequence (T = 0 launches
+ * nothing and looks at nothing). */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 
 moe_status_t moe_balance_loss_workspace_size(int64_t T, int E, int S, size_t* bytes);

@@ -356,3 +356,36 @@ def test_infinite_logits_of_sigmoids():
                                               balance_coef=0.5, z_coef=zc)
             assert ((g[a:b].double() - d).abs() <= bound).all()
     assert abs(loss[0].item() - total) <= total * (rel + 2.0 ** -18) and loss[1].item() == 0.0
+
+
+@pytest.mark.parametrize("T,E,cuts", [
+    (100, 16, [0, 50, 30, 100]), (100, 16, [0, 10, 5, 100]), (100, 16, [0, 100, 40]),
+    (128, 256, [0, 128, 200]), (128, 256, [0, 128, -1]), (128, 256, [-7, 0, 0, 128]),
+    (1, 1, [0, 1, 0, 1]), (3000, 64, [0, 1500, 1499, 1500, 3000])])
+def test_backward_reports_every_bad_offset(T, E, cuts):
+    """Also those of sequences that no token is in."""
+    x = torch.randn((T, E), generator=gen(21), device="cuda")
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    counts = torch.zeros((len(cuts) - 1, E), dtype=torch.int32, device="cuda")
+    assert moe.moe_device_status() == 0
+    moe.moe_balance_loss_backward(x, counts, 1, seq_offsets=off)
+    assert moe.moe_device_status() == 6
+    good = off.clamp(0, T).cummax(0).values.to(torch.int32)
+    moe.moe_balance_loss_backward(x, counts, 1, seq_offsets=good)
+    assert moe.moe_device_status() == 0
+
+
+def test_backward_reports_one_of_many_offsets():
+    T, E, S = 2000, 8, 300000
+    x = torch.randn((T, E), generator=gen(22), device="cuda")
+    off = torch.full((S + 1,), T, dtype=torch.int32, device="cuda")
+    off[:T] = torch.arange(T, device="cuda")
+    counts = torch.ones((S, E), dtype=torch.int32, device="cuda")
+    want = moe.moe_balance_loss_backward(x, counts, 1, seq_offsets=off)
+    assert moe.moe_device_status() == 0
+    for at in (S, S - 1, S // 2, T + 1):
+        bad = off.clone()
+        bad[at] = T + 1
+        got = moe.moe_balance_loss_backward(x, counts, 1, seq_offsets=bad)
+        assert moe.moe_device_status() == 6
+        assert got.shape == want.shape

@@ -442,6 +442,12 @@ balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restr
                         uint32_t* __restrict__ status) {
     constexpr int kSide = 32 / G;                     // rows of a warp at once
     constexpr bool kAhead = V <= 16;                  // registers for the next rows
+    // all the offsets, a thread one or few: rows' walks below step over sequences without tokens
+    bool bad = false;
+    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < seq.S;
+         i += int64_t(gridDim.x) * kThreads)
+        bad |= seq.bad(int(i));
+    if (bad && status) atomicExch(status, uint32_t(MOE_ERR_DEVICE_CHECK));
     const int lane = threadIdx.x % G, side = threadIdx.x % 32 / G;
     // a warp's rows are one run
     const int64_t first = (int64_t(blockIdx.x) * kWarps + threadIdx.x / 32) * kSide * rounds;
@@ -457,7 +463,6 @@ balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restr
     const float zc = 2.0f * z_coef * g1 / float(max64(seq.at(seq.S) - seq.at(0), 1));
     int s = seq.find(min64(first + side, last - 1));
     int64_t begin = 0, end = -1;                      // of sequence s
-    bool bad = false;
     Row<G, V, VEC> a;
     for (int64_t t0 = first; t0 < last; t0 += kSide) {
         const int64_t t = t0 + side;
@@ -490,7 +495,6 @@ balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restr
             const float f = balance_coef * g0 / (float(seq.S) * float(k)) / n / n;
 #pragma unroll
             for (int i = 0; i < V; ++i) a.at(i) = float(int64_t(c[i]) * E - total) * f;
-            bad |= seq.bad(s);
         }
         Scores<G, V, VEC> sc = row_scores<G, V, VEC, SIGMOID>(row);
         Row<G, V, VEC>& p = SIGMOID ? sc.sig : sc.u;
@@ -511,7 +515,6 @@ balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restr
         }
         if (t < last) row.store(grad + t * E, E, lane);
     }
-    if (bad && status) atomicExch(status, uint32_t(MOE_ERR_DEVICE_CHECK));
 }
 
 // ----------------------------------------------------------------- host side
