@@ -680,7 +680,8 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  * [E, 2I, H/2] packed with gate_up, w_down_q [E, H, I/2] without.  H and I multiples
  * of 64.  Workspace: moe_grouped_swiglu_fp4_workspace_size bytes (hidden's codes and
  * scales).  Both workspaces may hold anything; calls that share one must not overlap on
- * the GPU.  Their sizes follow from the arguments and the GPU's number of SMs.
+ * the GPU.  Their sizes follow from the arguments and do not fall as M grows: that of the
+ * largest call serves those of fewer rows.
  * Both products: offsets outside [0, M], or that decrease, leave MOE_ERR_DEVICE_CHECK in the
  * workspace status and y as it was. */
 moe_status_t moe_quantize_fp4(const void* x, moe_dtype_t dtype, int64_t T, int64_t H, int block,

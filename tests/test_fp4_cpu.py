@@ -126,3 +126,14 @@ def test_worked_values():
     assert sorted(at.view(-1).tolist()) == sorted(set(at.view(-1).tolist()))
     assert at[0, :5].tolist() == [0, 1, 2, 3, 512] and at[33, 0] == 20 and at[128, 0] == 4096
     assert f4.in_turn(128)[[0, 63, 64, 128]].tolist() == [0, 63, 128, 64]
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("E,H,I", [(1, 4096, 4096), (8, 512, 1408), (64, 7168, 2048), (256, 7168, 2048),
+                                   (300, 2048, 1024)])
+def test_workspace_sizes_do_not_fall(E, H, I, block):
+    """One workspace, of the largest call, serves every call of fewer rows."""
+    step = lambda f: [f(M) for M in [*range(0, 1300), *range(1300, 20000, 97), 65536, 1 << 20]]
+    for sizes in (step(lambda M: moe.moe_grouped_matmul_fp4_workspace_size(M, E, I, H, block)),
+                  step(lambda M: moe.moe_grouped_swiglu_fp4_workspace_size(M, E, H, I, block))):
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))

@@ -591,3 +591,28 @@ def test_negative_zeros_keep_their_sign(dtype, block, g):
     codes, _, _ = f4.quantize(w[0], block, 1.0 if g is None else g)
     q, _ = moe.moe_pack_fp4(w, block, global_scale=scalar(g))
     assert torch.equal(f4.unpairs(q[0]), codes)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("E,H,I", [(1, 512, 512), (4, 1024, 2048)])
+def test_one_workspace_for_calls_of_fewer_rows(E, H, I, block):
+    """That of 4096 rows, through tiles of 256, 128 and 32 rows."""
+    most = 4096
+    xq, xs, _ = fp4_rows(most, H, block, 1)
+    up, us, ug, _ = fp4_weights(E, 2 * I, H, block, 2, gate_up=True)
+    down, ds, dg, _ = fp4_weights(E, H, I, block, 3)
+    n = moe.moe_grouped_swiglu_fp4_workspace_size(most, E, H, I, block)
+    n2 = moe.moe_grouped_matmul_fp4_workspace_size(most, E, 2 * I, H, block)
+    ws, ws2 = (torch.full((v,), 0xFF, dtype=torch.uint8, device="cuda") for v in (n, n2))
+    for M in (4096, 2048, 2047, 1025, 1024, 513, 300, 129, 128, 65, 64, 33, 7, 1, 0):
+        off = segments("ragged", M, E, M)
+        args = (xq[:M], xs[:M], up, us, down, ds, off, block)
+        want = moe.moe_grouped_swiglu_fp4(*args, alpha_up=ug, alpha_down=dg)
+        got = moe.moe_grouped_swiglu_fp4(*args, alpha_up=ug, alpha_down=dg, workspace=ws)
+        assert torch.equal(want.view(torch.int16), got.view(torch.int16))
+        assert moe.moe_workspace_status(ws) == 0
+        args = (xq[:M], xs[:M], up, us, off, block)
+        want = moe.moe_grouped_matmul_fp4(*args, alpha=ug)
+        got = moe.moe_grouped_matmul_fp4(*args, alpha=ug, workspace=ws2)
+        assert torch.equal(want.view(torch.int16), got.view(torch.int16))
+        assert moe.moe_workspace_status(ws2) == 0

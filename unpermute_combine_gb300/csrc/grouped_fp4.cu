@@ -913,6 +913,13 @@ moe_status_t launch(const void* x_q, const void* w_q, Fp4Args a, cudaStream_t s)
                ? launch_status() : MOE_ERR_CUDA;
 }
 
+// May pairs be the choice for M rows, or fewer?  Where M rows make no more tiles of 128 rows
+// than of 256, blocks alone have no more rounds than pairs and a shorter stage.
+bool pairs_pay(int64_t M, int E) {
+    if (E > Shape<256, 16>::kExperts) return false;
+    return E == 1 ? M > 128 : M / 128 > (E + 1) / 2;
+}
+
 // Rows of a tile for products of E experts, M rows, and for each an N and a K (nothing for a
 // second of 0): those of the least estimated time in us.  The segments are known on the
 // device alone, so that every expert is taken to have rows, and half a tile to be lost on
@@ -932,7 +939,7 @@ int tile_rows(int64_t M, int E, int64_t N0, int64_t K0, int64_t N1, int64_t K1) 
     };
     const int sms = sm_count();
     const double few = time(32, 128, sms, 0.22), some = time(128, 128, sms, 0.32);
-    const double many = E <= Shape<256, 16>::kExperts
+    const double many = pairs_pay(M, E)
                             ? 2.0 + time(256, 256, sms > 1 ? sms / 2 : 1, 0.38) : some + 1.0;
     if (few <= some && few <= many) return 32;
     return some <= many ? 128 : 256;
@@ -1003,22 +1010,25 @@ using namespace moe;
 
 namespace {
 
-// A product's workspace: the status, and for pairs the rows' packed scales.
-size_t matmul_bytes(int64_t M, int E, int64_t K, int block, int rows) {
-    return kWsAlign + (rows == 256 ? align_up(size_t(packed_rows_bytes(M, E, K, block, BM)), kWsAlign) : 0);
+// Workspaces have room for what any tile that M rows or fewer may be given needs, so that the
+// largest call's serves the smaller ones.  A product's: the status, and where pairs may be
+// chosen the rows' packed scales.
+size_t matmul_bytes(int64_t M, int E, int64_t K, int block) {
+    return kWsAlign +
+           (pairs_pay(M, E) ? align_up(size_t(packed_rows_bytes(M, E, K, block, BM)), kWsAlign) : 0);
 }
 
-// The layer's: besides, the hidden rows' codes and their packed scales.
+// The layer's: besides, the hidden rows' codes and their packed scales, of which tiles of 32
+// rows have the most blocks.
 struct LayerParts {
     size_t hidden_q, hidden_scales, bytes;
 };
 
-LayerParts layer_parts(int64_t M, int E, int64_t H, int64_t I, int block, int rows) {
+LayerParts layer_parts(int64_t M, int E, int64_t H, int64_t I, int block) {
     LayerParts p;
-    p.hidden_q = matmul_bytes(M, E, H, block, rows);
+    p.hidden_q = matmul_bytes(M, E, H, block);
     p.hidden_scales = p.hidden_q + align_up(size_t(M) * size_t(I / 2), kWsAlign);
-    p.bytes = p.hidden_scales +
-              align_up(size_t(packed_rows_bytes(M, E, I, block, rows == 32 ? 32 : BM)), kWsAlign);
+    p.bytes = p.hidden_scales + align_up(size_t(packed_rows_bytes(M, E, I, block, 32)), kWsAlign);
     return p;
 }
 
@@ -1029,7 +1039,7 @@ extern "C" moe_status_t moe_grouped_matmul_fp4_workspace_size(int64_t M, int E, 
     if (!bytes) return MOE_ERR_INVALID_ARG;
     const moe_status_t st = check_product(M, E, N, K, block);
     if (st != MOE_OK) return st;
-    *bytes = M > 0 ? matmul_bytes(M, E, K, block, tile_rows(M, E, N, K, 0, 0)) : kWsAlign;
+    *bytes = matmul_bytes(M, E, K, block);
     return MOE_OK;
 }
 
@@ -1047,8 +1057,7 @@ extern "C" moe_status_t moe_grouped_matmul_fp4(const void* x_q, const void* x_sc
     if (!aligned16(x_q) || !aligned16(w_q) || !aligned16(w_scales) || !aligned16(y) ||
         !aligned(alpha, 4) || !aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
-    const int rows = M > 0 ? tile_rows(M, E, N, K, 0, 0) : 32;
-    if (!workspace_ok(workspace, workspace_bytes, matmul_bytes(M, E, K, block, rows)))
+    if (!workspace_ok(workspace, workspace_bytes, matmul_bytes(M, E, K, block)))
         return MOE_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     WsHeader* header = static_cast<WsHeader*>(workspace);
@@ -1057,6 +1066,7 @@ extern "C" moe_status_t moe_grouped_matmul_fp4(const void* x_q, const void* x_sc
     const Fp4Args a{offsets, M, E, int(K), N, 0, static_cast<const uint8_t*>(x_scales), 0,
                     static_cast<const uint8_t*>(w_scales), alpha, y, nullptr, nullptr, header, false};
     uint8_t* packed = static_cast<uint8_t*>(workspace) + kWsAlign;
+    const int rows = tile_rows(M, E, N, K, 0, 0);
     return block == 16 ? first_product<16, kPlain>(rows, x_q, w_q, a, packed, s)
                        : first_product<32, kPlain>(rows, x_q, w_q, a, packed, s);
 }
@@ -1066,7 +1076,7 @@ extern "C" moe_status_t moe_grouped_swiglu_fp4_workspace_size(int64_t M, int E, 
     if (!bytes) return MOE_ERR_INVALID_ARG;
     const moe_status_t st = check_layer(M, E, H, I, block);
     if (st != MOE_OK) return st;
-    *bytes = M > 0 ? layer_parts(M, E, H, I, block, tile_rows(M, E, 2 * I, H, H, I)).bytes : kWsAlign;
+    *bytes = M > 0 ? layer_parts(M, E, H, I, block).bytes : kWsAlign;
     return MOE_OK;
 }
 
@@ -1087,8 +1097,7 @@ extern "C" moe_status_t moe_grouped_swiglu_fp4(
         !aligned(alpha_down, 4) || !aligned(hidden_scale, 4) || !aligned(offsets, 4) ||
         (block == 32 && hidden_scale))
         return MOE_ERR_INVALID_ARG;
-    const int rows = M > 0 ? tile_rows(M, E, 2 * I, H, H, I) : 32;
-    const LayerParts parts = layer_parts(M, E, H, I, block, rows);
+    const LayerParts parts = layer_parts(M, E, H, I, block);
     if (!workspace_ok(workspace, workspace_bytes, M > 0 ? parts.bytes : kWsAlign))
         return MOE_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1096,6 +1105,7 @@ extern "C" moe_status_t moe_grouped_swiglu_fp4(
     if (M == 0)
         return cudaMemsetAsync(header, 0, sizeof *header, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int rows = tile_rows(M, E, 2 * I, H, H, I);
     const Fp4Args up{offsets, M, E, int(H), 2 * I, 0, static_cast<const uint8_t*>(x_scales), 0,
                      static_cast<const uint8_t*>(w_up_scales), alpha_up, ws + parts.hidden_q,
                      ws + parts.hidden_scales, hidden_scale, header, false};
