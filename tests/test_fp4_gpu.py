@@ -1,4 +1,8 @@
 """Rows, weights and products in e2m1 against float64."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -616,3 +620,32 @@ def test_one_workspace_for_calls_of_fewer_rows(E, H, I, block):
         got = moe.moe_grouped_matmul_fp4(*args, alpha=ug, workspace=ws2)
         assert torch.equal(want.view(torch.int16), got.view(torch.int16))
         assert moe.moe_workspace_status(ws2) == 0
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_first_calls_of_a_process_are_captured(block):
+    """What is looked up once, for each kernel by itself, is looked up under a capture."""
+    code = f"""
+import torch, test_fp4_gpu as t, unpermute_combine_gb300 as moe
+M, E, H, I = 8000, 2, 512, 1024
+block = {block}
+xq, xs, _ = t.fp4_rows(M, H, block, 1)
+up, us, ug, _ = t.fp4_weights(E, 2 * I, H, block, 2, gate_up=True)
+down, ds, dg, _ = t.fp4_weights(E, H, I, block, 3)
+off = t.segments("ragged", M, E, 4)
+def step():
+    return (moe.moe_grouped_swiglu_fp4(xq, xs, up, us, down, ds, off, block, alpha_up=ug, alpha_down=dg),
+            moe.moe_grouped_matmul_fp4(xq, xs, up, us, off, block, alpha=ug))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
+assert all(moe.moe_workspace_status(a._moe_workspace) == 0 for a in (*got, *want))
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -865,8 +865,9 @@ bool make_map_packed(CUtensorMap* map, const void* base, int64_t bytes, int part
            CUDA_SUCCESS;
 }
 
-// Clusters of two that the current device runs at once (one block an SM), looked up once.
-int pair_count(const void* kernel, int smem) {
+// Clusters of two of this kernel that the current device runs at once, looked up once.
+template <int ROWS, int BLOCK, int EPI, bool PACKED>
+int pair_count() {
     static std::mutex m;
     static int cached[64] = {};
     int dev = 0;
@@ -876,7 +877,7 @@ int pair_count(const void* kernel, int smem) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(sm_count()) / 2 * 2);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = size_t(smem);
+        cfg.dynamicSmemBytes = Shape<ROWS, BLOCK>::kSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -884,6 +885,7 @@ int pair_count(const void* kernel, int smem) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
+        const auto kernel = (const void*)grouped_fp4_kernel<ROWS, BLOCK, EPI, PACKED>;
         if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
         cached[dev] = n < sm_count() / 2 ? n : sm_count() / 2;
     }
@@ -906,7 +908,8 @@ moe_status_t launch(const void* x_q, const void* w_q, Fp4Args a, cudaStream_t s)
         return MOE_ERR_CUDA;
     const auto kernel = grouped_fp4_kernel<ROWS, BLOCK, EPI, PACKED>;
     if (!opt_in_smem((const void*)kernel, S::kSmem)) return MOE_ERR_CUDA;
-    const int blocks = S::CTAS == 2 ? 2 * pair_count((const void*)kernel, S::kSmem) : sm_count();
+    int blocks = sm_count();
+    if constexpr (S::CTAS == 2) blocks = 2 * pair_count<ROWS, BLOCK, EPI, PACKED>();
     if (blocks < 1) return MOE_ERR_CUDA;
     a.n_tiles = int((a.N + S::BN - 1) / S::BN);
     return launch_dependent(kernel, unsigned(blocks), kThreads, S::kSmem, s, m, a) == cudaSuccess
