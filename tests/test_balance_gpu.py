@@ -389,3 +389,36 @@ def test_backward_reports_one_of_many_offsets():
         got = moe.moe_balance_loss_backward(x, counts, 1, seq_offsets=bad)
         assert moe.moe_device_status() == 6
         assert got.shape == want.shape
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shift", [80.0, -80.0, -2000.0, 3000.0])
+def test_shifted_rows_are_as_exact_as_near_ones(shift, score):
+    """Rows whose exponentials' sum leaves float's middle are shifted by their largest: the
+    scores' error goes by how far a row's logits lie from one another, not from 0."""
+    T, E, k = 128, 64, 2
+    x = torch.randn((T, E), generator=gen(24), device="cuda") + shift
+    idx = choices(x, k, 6)
+    how = dict(score=score, balance_coef=0.5, z_coef=0.0)
+    loss, counts, mean = moe.moe_balance_loss(x, idx, **how)
+    want, wc, wm, wg = reference(x, idx, None, score, 0.5, 0.0, E)
+    assert torch.equal(counts, wc)
+    # With v = x less the row's largest, in steps of 2^-24: v is off by |v|, v log2 e by
+    # 2 |v| (log2 e itself and the product, of which ln 2 reaches the exponential), 2^x by 4,
+    # twice: the element's and the sum's; the sum by log2 64 + 2 additions, 1/x and the product
+    # by 2 + 1.  A sigmoid of x > 0 adds 2 |x| e^-x, its exponential's error, and 3.
+    v = spread(x)
+    rel = (2 * (3 * v + 4) + 8 + 3 + 6) * 2.0 ** -24
+    # sums: eight rows of a chunk of 32 side by side, then warps, chunks
+    sums = rel + (4 + 8 + 8 + 2) * 2.0 ** -24
+    assert ((mean.double() - wm).abs() <= wm * sums).all()
+    assert abs(loss[0].item() - want[0].item()) <= want[0].item() * (sums + 10 * 2.0 ** -24)
+    got = moe.moe_balance_loss_backward(x, counts, k, **how)
+    f = wc[0].double() * E / (k * T)
+    most = (f - f.mean()).abs().max()
+    p = torch.softmax(torch.nn.functional.logsigmoid(x.double()) if score == "sigmoid" else x.double(), 1)
+    bound = p * most * (0.5 / T) * (4 * rel)
+    if score == "sigmoid":                          # times 1 - sigmoid, an exponential of x itself
+        keep = torch.sigmoid(-x.double())
+        bound = bound * keep + wg[0].abs() * (3 * abs(shift) + 20) * 2.0 ** -24 + 1e-37
+    assert ((got.double() - wg[0]).abs() <= bound + wg[0].abs() * 2.0 ** -22).all()

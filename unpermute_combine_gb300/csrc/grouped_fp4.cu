@@ -364,6 +364,7 @@ __global__ void __cluster_dims__(ROWS == 256 ? 2 : 1, 1, 1) __launch_bounds__(kT
 grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
     using S = Shape<ROWS, BLOCK>;
     constexpr int CTAS = S::CTAS, BN = S::BN, kStages = S::kStages, kRows = S::kRows;
+    static_assert(PACKED || CTAS == 1, "pairs take packed scales");
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[kStages];      // (the leader's are used)
     __shared__ __align__(8) uint64_t empty_bar[kStages];
@@ -384,7 +385,7 @@ grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
 
     if (threadIdx.x == 32) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_addr(&full_bar[s]), PACKED ? 1 : 1 + CTAS);   // the copies, the rows' scales
+            mbar_init(smem_addr(&full_bar[s]), PACKED ? 1 : 2);    // the copies, the rows' scales
             mbar_init(smem_addr(&empty_bar[s]), 1);
         }
         mbar_init(smem_addr(&acc_full_bar[0]), 1);
@@ -612,22 +613,16 @@ grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
             mbar_wait(smem_addr(&drain_bar), 0);
         }
     } else if (!PACKED && (warp == 2 || warp == 3)) {
-        // ------------------------------------------------------ scales of the rows
-        if (args.after_own) wait_for_predecessor();
+        // -------------------------------- scales of the rows (in a call's first kernel)
         uint32_t it = warp - 2;
         int t = first, ks = warp - 2;
         Tile at{};
-        auto own = [&] {                          // this block's part of tile t
-            at = tile_of(t);
-            at.rows = rows_of(at, rank);
-            at.row += rank * BM;
-        };
         auto settle = [&] {                       // (t, ks) of the stage `it`
             bool moved = false;
             while (ks >= k_stages) ks -= k_stages, t += step, moved = true;
-            if (moved && t < total) own();
+            if (moved && t < total) at = tile_of(t);
         };
-        if (t < total) own();
+        if (t < total) at = tile_of(t);
         settle();
         auto row_scales = [&](const Tile& of, int k) {
             return load_scales<BLOCK>(args.x_scales, args.n_rows, args.K, args.x_vec, of.row, of.rows, k,
@@ -650,7 +645,7 @@ grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
                                 "r"(now.w[2][p]), "r"(now.w[3][p]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) arrive_at<CTAS>(full_at(it));
+            if (lane == 0) mbar_arrive(full_at(it));
             it += 2;
         }
     } else if (warp >= 4 && warp < 4 + S::kEpiWarps) {
