@@ -227,8 +227,10 @@ struct Pieces {                         // the workspace behind its header
 
 // 131072 x 256, sigmoid: 36 us (3.7 TB/s), four blocks an SM in one wave, 146 instructions a
 // row and 64% of the issue slots; with 78 registers, three blocks and two waves, 51.
+// (The bound is the wave's: without it the compiler took 77 registers for the search past empty
+// sequences, three blocks an SM and 48 us.)
 template <int G, int V, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : V <= 16 ? 2 : 0)
 balance_pieces_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                       Sequences seq, int E, int k, int64_t chunk, Pieces out) {
     constexpr int kSide = 32 / G, kStep = kWarps * kSide;      // rows of a warp, of the block at once
@@ -246,7 +248,10 @@ balance_pieces_kernel(const float* __restrict__ logits, const int32_t* __restric
         const int64_t begin = seq.at(s);
         if (begin >= last) break;
         const int64_t a = max64(begin, first), b = min64(seq.at(s + 1), last);
-        if (a >= b) continue;
+        if (a >= b) {                   // past sequences without tokens, of which there may be many
+            s = max(s, seq.find(a) - 1);
+            continue;
+        }
         // the next rows load while these are worked on
         const int n = int(b - a), r1 = warp * kSide;
         const float* rows = logits + a * E;
@@ -480,7 +485,9 @@ balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restr
         // the sequence's counts less their mean (whole numbers), over n^2
         const bool fresh = end < 0 || (t >= end && s + 1 < seq.S);
         if (__any_sync(0xFFFFFFFFu, fresh)) {
-            while (s + 1 < seq.S && seq.at(s + 1) <= t) ++s;
+            // the next one; past sequences without tokens, of which there may be many, by a search
+            auto begun = [&] { return s + 1 < seq.S && seq.at(s + 1) <= t; };
+            if (begun() && (++s, begun())) s = seq.find(t);
             begin = seq.at(s), end = seq.at(s + 1);
             int c[V], total = 0;
 #pragma unroll
