@@ -669,7 +669,8 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  * they were.  x_q [M, K/2], x_scales [M, K/block] as the quantizers leave them; w_q,
  * w_scales as moe_pack_fp4 does (gate_up = 0); alpha [E] float (NULL: ones), the
  * product of the two sides' g; offsets [E+1] int32 on the device; y [M,N].  K a
- * multiple of 32, N of 8, E <= 1024 (else MOE_ERR_UNSUPPORTED); x_q, w_q, w_scales, y
+ * multiple of 32, N of 8, E <= 1024 (else MOE_ERR_UNSUPPORTED; long prefills of more than
+ * 256 experts take the slower tiles of single blocks); x_q, w_q, w_scales, y
  * 16-byte aligned.  Workspace: moe_grouped_matmul_fp4_workspace_size bytes.
  *
  * moe_grouped_swiglu_fp4: the experts' network, up to any number of rows:
@@ -683,7 +684,7 @@ moe_status_t moe_balance_loss_backward(const float* logits, const int32_t* count
  * the GPU.  Their sizes follow from the arguments and do not fall as M grows: that of the
  * largest call serves those of fewer rows.
  * Both products: offsets outside [0, M], or that decrease, leave MOE_ERR_DEVICE_CHECK in the
- * workspace status and y as it was. */
+ * workspace status and y as it was (M = 0 launches nothing and looks at nothing). */
 moe_status_t moe_quantize_fp4(const void* x, moe_dtype_t dtype, int64_t T, int64_t H, int block,
                               const float* global_scale, void* x_q, void* scales, void* stream);
 

@@ -204,6 +204,7 @@ __device__ __forceinline__ Scores<G, V, VEC> row_scores(const Row<G, V, VEC>& ro
         const float again = group_sum<G>(s.u.sum());
         if (odd) sum = again;
     }
+    // (__logf is off by 2^-21.4 near 1, about as far as the sum is: 2^-22 and its additions)
     s.lse = none ? 0.0f : shift + __logf(sum);
     s.inv = none ? 0.0f : rcp_ftz(sum);
     if (SIGMOID) {
@@ -225,10 +226,11 @@ struct Pieces {                         // the workspace behind its header
     int32_t* counts;                    // [pieces][E]
 };
 
-// 131072 x 256, sigmoid: 36 us (3.7 TB/s), four blocks an SM in one wave, 146 instructions a
-// row and 64% of the issue slots; with 78 registers, three blocks and two waves, 51.
-// (The bound is the wave's: without it the compiler took 77 registers for the search past empty
-// sequences, three blocks an SM and 48 us.)
+// 131072 x 256: 27 us with the sigmoid and 26 with the softmax where nothing else is in L2 (5.1
+// TB/s of logits and choices), 33 for both behind a gradient whose stores leave L2 meanwhile.
+// With the sigmoid 143 instructions of a warp a row; the softmax's are fewer and take as long:
+// neither the issue slots (62%) nor memory is full.  Rows of 8 values a lane have four blocks an SM, all chunks in one wave, which the
+// bound keeps: with 77 or 78 registers, three blocks and two waves, it is 15 us more.
 template <int G, int V, bool VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : V <= 16 ? 2 : 0)
 balance_pieces_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
@@ -340,8 +342,9 @@ __device__ __forceinline__ float block_sum(float v, float* s_part) {
 
 // Block (s, J experts): adds the pieces of sequence s, 256 / J of them side by side and four
 // of each in flight; the block that ends last adds up the losses.  In float32: chains of
-// float64 additions, slow on this GPU, were 12 us of a join of 256 pieces.  Sums of at most
-// 1024 pieces over 32 threads, 4 at a time, are off by 2^-20.
+// float64 additions, slow on this GPU, were 12 us of a join of 256 pieces.  A sequence has
+// kMostChunks pieces at most: chains of 19 additions over 32 threads, or 76 over the 8 of many
+// sequences, off by 2^-19 or 2^-17.6 at the worst.
 constexpr int kJoin = 8;                // few sequences; many: 32 experts a block
 
 template <int J>
@@ -437,8 +440,8 @@ balance_join_kernel(Sequences seq, int E, int k, int64_t chunk, int chunks, floa
 
 // --------------------------------------------------------------- backward
 
-// 131072 x 256, sigmoid: 46 us (5.8 TB/s in and out), 235 instructions a row and 58% of the
-// issue slots.
+// 131072 x 256: 47 us with the sigmoid (5.7 TB/s in and out, 236 instructions of a warp a row and
+// 57% of the issue slots), 44 with the softmax (6.1 TB/s, 201 and 56%).
 template <int G, int V, bool VEC, bool SIGMOID, bool ADD>
 __global__ void __launch_bounds__(kThreads)
 balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ counts,

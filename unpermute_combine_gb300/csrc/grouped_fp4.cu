@@ -15,7 +15,8 @@
 //               more through L2, copied twice the scales for the same MMAs and ran at
 //               3/4 of the rate.
 //   ROWS = 128  128 x 128 by one block: less work, which pairs would spread over fewer
-//               SMs, and more experts than a pair's schedule has room for.
+//               SMs, and more experts than a pair's schedule has room for (65536 rows, H = 7168,
+//               I = 2048, blocks of 32: 256 experts 1320 us, 257 by such blocks 1890).
 //   ROWS = 32   32 x 128, still MMAs of 128 rows, whose other rows read whatever lies
 //               behind the 32: a few rows an expert, where the weights' way in is what
 //               counts and rows' slots would take the place of weights in flight.
@@ -34,8 +35,8 @@
 // Persistent blocks take tiles in the order of grouped_swiglu.cu: experts, in an
 // expert the column tiles, in those the row tiles.
 // Measured: 16384 rows of four experts, 7168 x 7168, 252 us or 6.6 PFLOP/s, the tensor pipe
-// 80% busy, until the card's power holds it at 290 us; 65536 rows through 64 experts, H =
-// 7168, I = 2048, 930 us; 512 rows through them 236 us, 6.7 TB/s of weights; one row, 7168 x
+// 80% busy, until the card's power holds it at 280-295 us; 65536 rows through 64 experts, H =
+// 7168, I = 2048, 924 us; 512 rows through them 236 us, 6.7 TB/s of weights; one row, 7168 x
 // 2048, 8 us, most of it latency (offsets 0.8, the first tile 1.7, eight stages 2.4).
 // Tensor memory has 512 columns: a pair's two accumulators of 256 overlap, so that
 // stages' scales fit beside them; the epilogue takes the shared columns first.
